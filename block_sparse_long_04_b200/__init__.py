@@ -56,6 +56,37 @@ SIGNATURES = {
                                 _P, _P, _Z, _P]),
 }
 
+# structs of the decoding operators; fields mirror include/xattn.h
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_m", ctypes.c_longlong), ("heads", _I)]
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("pos", _P), ("inv_freq", _P), ("sections", _I * 4), ("axes", _I),
+                ("interleaved", _I), ("pos_batch", _I)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k_pages", _P), ("v_pages", _P), ("k_scale", _P), ("v_scale", _P), ("acc", _P),
+                ("ordinal", _P), ("page_table", _P), ("lens", _P), ("B", _I), ("Hkv", _I),
+                ("C", _I), ("page", _I), ("num_pages", _I), ("max_pages", _I), ("kv_type", _I)]
+
+
+_PH, _PR, _PC = (ctypes.POINTER(t) for t in (_Heads, _Rotary, _Cache))
+SIGNATURES.update({
+    "xattn_rope": (_I, [_PH, _PH, _PR, _I, _I, _I, _I, _PH, _PH, _P]),
+    "xattn_cache_append": (_I, [_PH, _PH, _PC, _I, _P, _P, _P]),
+    "xattn_rope_append": (_I, [_PH, _PH, _PH, _PR, _PC, _I, _P, _P, _PH, _P]),
+    "xattn_decode_workspace_size": (_Z, [_PC, _I, _I]),
+    "xattn_decode_attn": (_I, [_PH, _PC, _F, _P, _P, _P, _P, _Z, _P]),
+    "xattn_cache_evict_workspace_size": (_Z, [_PC, _I]),
+    "xattn_cache_evict": (_I, [_PC, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
+})
+
+XATTN_KV_BF16, XATTN_KV_E4M3 = 0, 1
+XATTN_ROPE_MAX_AXES = 4
+
 XATTN_PATTERN_ANTIDIAGONAL, XATTN_PATTERN_DIAGONAL = 0, 1
 XATTN_SELECT_THRESHOLD, XATTN_SELECT_TOPK, XATTN_SELECT_RATIO = 0, 1, 2
 
@@ -357,3 +388,258 @@ def xattn_prefill(Q, K, V, tau, stride: int, causal: bool, bufs: Buffers,
     xattn_sparse_attn(Q, K, V, bufs.row_ptr, bufs.col_idx, causal, sa, bufs.O, bufs.lse, block,
                       stream)
     return bufs.O
+
+
+# ----------------------------------------------------- decoding operators
+def _device_of(*ts):
+    """The one device of the given tensors (None entries aside)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors are on different devices ({dev} and {t.device})")
+    return dev
+
+
+def _call(name: str, dev, stream, *args) -> None:
+    """Calls a C entry point on `stream` (default: the current one of `dev`), with `dev`
+    the current device."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            rc = getattr(_lib, name)(*args, _stream(stream))
+    else:
+        rc = getattr(_lib, name)(*args, _stream(stream))
+    if rc != XATTN_OK:
+        raise XAttnError(rc, name)
+
+
+def _heads(t: torch.Tensor, what: str, shape=None) -> _Heads:
+    """[B, H, M, C] bf16 rows at any strides with contiguous elements."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be bfloat16")
+    if t.dim() != 4 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}" +
+                         (f", {tuple(shape)} is wanted" if shape is not None else ", [B, H, M, C] is wanted"))
+    sb, sh, sm, sc = t.stride()
+    if sc != 1 and t.shape[3] > 1:
+        raise ValueError(f"the elements of a row of {what} must be contiguous")
+    B, H, M, _ = t.shape
+    # the stride of a dimension of size 1 means nothing and need not be aligned
+    return _Heads(t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, sm if M > 1 else 0, H)
+
+
+def _want(t, what: str, dtype, shape) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} is wanted")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+class Rotary:
+    """Rotary positions: which pairs of a row turn by which axis, and how fast.
+
+    inv_freq     fp64 CUDA tensor [pairs]
+    sections     pairs of each axis, e.g. (64,) for text, (16, 24, 24) for time, height, width
+    interleaved  pair p is (2p, 2p+1) instead of (p, p + pairs)
+    """
+
+    def __init__(self, inv_freq: torch.Tensor, sections, interleaved: bool = False):
+        sections = tuple(int(n) for n in sections)
+        if not 1 <= len(sections) <= XATTN_ROPE_MAX_AXES or min(sections) < 0:
+            raise ValueError(f"sections {sections}: 1 to {XATTN_ROPE_MAX_AXES} counts are wanted")
+        _want(inv_freq, "inv_freq", torch.float64, (sum(sections),))
+        _device_of(inv_freq)
+        self.inv_freq, self.sections, self.interleaved = inv_freq, sections, bool(interleaved)
+        self._sections = (_I * 4)(*sections)
+
+    @staticmethod
+    def make(sections, base: float = 10000.0, interleaved: bool = False, device="cuda") -> "Rotary":
+        """base^(-i/n) for the i-th of the n pairs of each axis."""
+        f = [base ** (-torch.arange(n, dtype=torch.float64) / n) for n in sections if n]
+        return Rotary(torch.cat(f).to(device), sections, interleaved)
+
+    def _struct(self, pos: torch.Tensor, B: int, M: int) -> _Rotary:
+        if pos.dim() == 2:
+            _want(pos, "pos", torch.int32, (M, len(self.sections)))
+            n = 1
+        else:
+            _want(pos, "pos", torch.int32, (B, M, len(self.sections)))
+            n = B
+        return _Rotary(pos.data_ptr(), self.inv_freq.data_ptr(), self._sections, len(self.sections),
+                       int(self.interleaved), n)
+
+
+class PagedCache:
+    """A paged key-value cache: the tensors of an xattn_cache (see include/xattn.h).
+
+    k_pages, v_pages  [num_pages, Hkv, page, C], bfloat16 or float8_e4m3fn
+    page_table        int32 [B, max_pages];  lens  int32 [B], slots in use
+    k_scale, v_scale  fp32 [Hkv], for float8_e4m3fn pages
+    acc, ordinal      fp32 / int32 [num_pages, Hkv, page], for eviction
+    The tensors are the caller's; the cache holds references and checks them once.
+    """
+
+    def __init__(self, k_pages, v_pages, page_table, lens, k_scale=None, v_scale=None, acc=None,
+                 ordinal=None):
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [num_pages, Hkv, page, C]")
+        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError("pages must be bfloat16 or float8_e4m3fn")
+        P, Hkv, page, C = k_pages.shape
+        B, max_pages = page_table.shape
+        e4m3 = k_pages.dtype == torch.float8_e4m3fn
+        _want(k_pages, "k_pages", k_pages.dtype, k_pages.shape)
+        _want(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
+        _want(page_table, "page_table", torch.int32, (B, max_pages))
+        _want(lens, "lens", torch.int32, (B,))
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to float8_e4m3fn pages")
+        if e4m3:
+            _want(k_scale, "k_scale", torch.float32, (Hkv,))
+            _want(v_scale, "v_scale", torch.float32, (Hkv,))
+        if acc is not None:
+            _want(acc, "acc", torch.float32, (P, Hkv, page))
+        if ordinal is not None:
+            _want(ordinal, "ordinal", torch.int32, (P, Hkv, page))
+        self.device = _device_of(k_pages, v_pages, page_table, lens, k_scale, v_scale, acc, ordinal)
+        self.k_pages, self.v_pages, self.page_table, self.lens = k_pages, v_pages, page_table, lens
+        self.k_scale, self.v_scale, self.acc, self.ordinal = k_scale, v_scale, acc, ordinal
+        self.B, self.Hkv, self.C, self.page = B, Hkv, C, page
+        self.num_pages, self.max_pages = P, max_pages
+        self.kv_type = XATTN_KV_E4M3 if e4m3 else XATTN_KV_BF16
+
+    @staticmethod
+    def allocate(B, Hkv, C, num_pages, max_pages, page=64, dtype=torch.bfloat16, eviction=False,
+                 k_scale=None, v_scale=None, device="cuda") -> "PagedCache":
+        """An empty cache (lens 0); page p of the pool is entry p of the table, row by row,
+        as far as the pool goes (-1 behind)."""
+        dev = torch.device(device)
+        table = torch.arange(B * max_pages, dtype=torch.int32, device=dev)
+        table = torch.where(table < num_pages, table, -1).view(B, max_pages)
+        pool = (num_pages, Hkv, page)
+        if dtype == torch.float8_e4m3fn:
+            k_scale = torch.ones(Hkv, device=dev) if k_scale is None else k_scale
+            v_scale = torch.ones(Hkv, device=dev) if v_scale is None else v_scale
+        return PagedCache(
+            torch.empty((*pool, C), dtype=dtype, device=dev),
+            torch.empty((*pool, C), dtype=dtype, device=dev),
+            table, torch.zeros(B, dtype=torch.int32, device=dev), k_scale, v_scale,
+            torch.zeros(pool, dtype=torch.float32, device=dev) if eviction else None,
+            torch.zeros(pool, dtype=torch.int32, device=dev) if eviction else None)
+
+    def _struct(self) -> _Cache:
+        return _Cache(self.k_pages.data_ptr(), self.v_pages.data_ptr(), _ptr(self.k_scale),
+                      _ptr(self.v_scale), _ptr(self.acc), _ptr(self.ordinal),
+                      self.page_table.data_ptr(), self.lens.data_ptr(), self.B, self.Hkv, self.C,
+                      self.page, self.num_pages, self.max_pages, self.kv_type)
+
+
+def xattn_rope(Q, K, pos, rotary: Rotary, Qo, Ko, inverse: bool = False, stream=None) -> None:
+    """Qo, Ko <- Q, K rotated by their positions (back, if inverse: also the gradient).
+
+    Q, Qo [B, Hq, M, C] and K, Ko [B, Hkv, M, C] (or both None) at any strides with
+    contiguous rows; pos int32 [M, axes] or [B, M, axes]. An output may be its input."""
+    dev = _device_of(Q, K, pos, rotary.inv_freq, Qo, Ko)
+    B, _, M, C = Q.shape
+    q, qo = _heads(Q, "Q"), _heads(Qo, "Qo", Q.shape)
+    if (K is None) != (Ko is None):
+        raise ValueError("K and Ko go together")
+    k = ko = None
+    if K is not None:
+        k, ko = _heads(K, "K", (B, K.shape[1], M, C)), _heads(Ko, "Ko", K.shape)
+    _call("xattn_rope", dev, stream, q, k, rotary._struct(pos, B, M), int(inverse), B, M, C, qo, ko)
+
+
+def _per_sequence(t, what: str, B: int):
+    if t is not None:
+        _want(t, what, torch.int32, (B,))
+    return _ptr(t)
+
+
+def xattn_cache_append(K, V, cache: PagedCache, n_new=None, seen=None, stream=None) -> None:
+    """The last n_new[b] (default: all T) slots of every sequence <- K, V [B, Hkv, T, C].
+    cache.lens already counts the new tokens; seen[b] (default: lens) counts every token
+    of the sequence, evicted ones too."""
+    dev = _device_of(K, V, cache.k_pages, n_new, seen)
+    shape = (cache.B, cache.Hkv, K.shape[2], cache.C)
+    _call("xattn_cache_append", dev, stream, _heads(K, "K", shape), _heads(V, "V", shape),
+          cache._struct(), shape[2], _per_sequence(n_new, "n_new", cache.B),
+          _per_sequence(seen, "seen", cache.B))
+
+
+def xattn_rope_append(Q, K, V, pos, rotary: Rotary, cache: PagedCache, Qo, n_new=None, seen=None,
+                      stream=None) -> None:
+    """xattn_rope of Q (into Qo) and K, and xattn_cache_append of the rotated K and of V,
+    in one launch."""
+    dev = _device_of(Q, K, V, pos, rotary.inv_freq, cache.k_pages, Qo, n_new, seen)
+    B, T = cache.B, K.shape[2]
+    shape = (B, cache.Hkv, T, cache.C)
+    _call("xattn_rope_append", dev, stream, _heads(Q, "Q", (B, Q.shape[1], T, cache.C)),
+          _heads(K, "K", shape), _heads(V, "V", shape), rotary._struct(pos, B, T), cache._struct(), T,
+          _per_sequence(n_new, "n_new", B), _per_sequence(seen, "seen", B),
+          _heads(Qo, "Qo", Q.shape))
+
+
+def xattn_decode_workspace_size(cache: PagedCache, Hq: int, weights: bool = False) -> int:
+    return int(_lib.xattn_decode_workspace_size(cache._struct(), int(Hq), int(weights)))
+
+
+def xattn_decode_attn(Q, cache: PagedCache, softmax_scale: float, O, workspace, lse=None,
+                      weights: bool = False, acc_out=None, stream=None) -> None:
+    """O <- attention of one query per sequence and head over the cache's slots in use.
+
+    Q and O [B, Hq, C] or [B, Hq, 1, C]; Q at any strides, O contiguous; lse fp32 [B, Hq].
+    weights adds every slot's softmax weight, summed over the query heads of its KV head,
+    to cache.acc, into acc_out (default: cache.acc itself)."""
+    dev = _device_of(Q, cache.k_pages, O, workspace, lse, acc_out)
+    q = _heads(Q.unsqueeze(2) if Q.dim() == 3 else Q, "Q", (cache.B, Q.shape[1], 1, cache.C))
+    _want(O, "O", torch.bfloat16, Q.shape)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, (cache.B, Q.shape[1]))
+    if weights:
+        if cache.acc is None:
+            raise ValueError("weights need a cache with acc")
+        if acc_out is None:
+            acc_out = cache.acc
+        else:
+            _want(acc_out, "acc_out", torch.float32, cache.acc.shape)
+    elif acc_out is not None:
+        raise ValueError("acc_out needs weights=True")
+    _want(workspace, "workspace", workspace.dtype, workspace.shape)
+    _call("xattn_decode_attn", dev, stream, q, cache._struct(), float(softmax_scale), O.data_ptr(),
+          _ptr(lse), _ptr(acc_out), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+
+
+def xattn_cache_evict_workspace_size(cache: PagedCache, budget: int) -> int:
+    return int(_lib.xattn_cache_evict_workspace_size(cache._struct(), int(budget)))
+
+
+def xattn_cache_evict(cache: PagedCache, budget: int, workspace, recent: int = 0, sink: int = 0,
+                      seen=None, acc_out=None, ord_out=None, stream=None) -> None:
+    """Keeps min(lens, budget) slots of every sequence and KV head, in slots 0..: those of the
+    `recent` last and `sink` first tokens, then the largest cache.acc. acc_out and ord_out
+    default to the cache's own. cache.lens is left to the caller: clamp it to budget after
+    the last layer that shares it."""
+    dev = _device_of(cache.k_pages, workspace, seen, acc_out, ord_out)
+    if cache.acc is None or cache.ordinal is None:
+        raise ValueError("eviction needs a cache with acc and ordinal")
+    if acc_out is None:
+        acc_out = cache.acc
+    else:
+        _want(acc_out, "acc_out", torch.float32, cache.acc.shape)
+    if ord_out is None:
+        ord_out = cache.ordinal
+    else:
+        _want(ord_out, "ord_out", torch.int32, cache.ordinal.shape)
+    _want(workspace, "workspace", workspace.dtype, workspace.shape)
+    _call("xattn_cache_evict", dev, stream, cache._struct(), int(budget), int(recent), int(sink),
+          _per_sequence(seen, "seen", cache.B), acc_out.data_ptr(), ord_out.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())

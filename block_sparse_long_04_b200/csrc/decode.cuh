@@ -1,0 +1,673 @@
+// Attention of one new token per sequence over a paged key-value cache.
+//
+//   o_h = sum_j softmax_j(scale q_h . k_j) v_j,  j over the slots < lens[b]
+//
+// Bound. Every cached byte is used once for 2 * Hq/Hkv flops per bf16 element, so HBM
+// sets the pace (4 to 16 flops per byte at the usual group sizes). The kernel's task is
+// to keep enough bytes in flight on every SM and to stay off everybody's critical path.
+//
+// Split. The tiles (64 keys) of all (sequence, kv head) items form one linear order,
+// which is cut into equal shares, one per CTA: ragged batches and single long sequences
+// load all SMs alike, and nothing has to be planned on the host. A CTA walks its share;
+// where an item ends inside it, the partial (maximum, sum, unnormalised output) goes to
+// the workspace. Items that one CTA covers alone are finished there, the others by
+// decode_join_kernel. CTA c and item i meet in at most one segment, and along the linear
+// order c + i grows, so c + i numbers the partials.
+//
+// One CTA (two per SM): warp 4 loads K and V tiles by TMA, one box per page part, into
+// a ring of stages; warps 0-3 own 16 of the tile's 64 keys each and run
+// independently (own maximum, sum and output) until the item's end. The products use
+// warp-level MMAs: with Hq/Hkv <= 16 query rows the tensor work is a few percent of what
+// even that path offers, while a tcgen05 tile (M = 128) would hold 8 to 32 useful rows
+// and pass P and O through shared memory and TMEM between the steps.
+// The 16 rows of an MMA hold 8 heads twice in the P V product: rows 0-7 take the rounded
+// weights, rows 8-15 what the rounding left (p - round(p)), so the weights enter
+// with 16 (bf16) or 22 (f16) bits at no extra instruction, and o is rounded once.
+//
+// e4m3 pages are widened to f16, which holds them exactly. q is scaled by a power of two
+// per head so that its largest element is in [1/2, 1]; below 2^-14 of that f16 loses
+// bits, an error of 2^-25 of the largest element, less than the fp32 sums'.
+//
+// Keys behind the end of a sequence inside its last page are masked, and their V rows
+// are zeroed in shared memory before use: 0 * NaN of a stale row would not be 0.
+// Every wait is bounded (sm100::mbar_wait).
+#pragma once
+#include <cuda_fp16.h>
+#include "common.cuh"
+#include "rope_append.cuh"
+#include "sm100.cuh"
+
+namespace xattn {
+
+constexpr int kDecTile = 64;          // keys per stage
+constexpr int kDecThreads = 160;      // four MMA warps, one TMA warp
+constexpr int kDecCtas = 296;         // 148 SMs x 2
+constexpr int kJoinThreads = 512;
+constexpr int kDecMaxGroup = 128;     // query heads per kv head
+
+struct DecodeParams {
+  CacheView cache;
+  const bf16* q;
+  long long q_sb, q_sh;
+  bf16* O;                 // [B, Hq, C]
+  float* lse;              // [B, Hq] or null
+  float* part_o;           // [partials][rows][C]
+  float2* part_ml;         // [partials][rows] (maximum in log2 units, sum)
+  int2* seg;               // [items] first and last CTA of the item
+  float* logits;           // [B, Hq, capacity] in log2 units, or null
+  float* acc_out;          // [num_pages, Hkv, page] or null
+  int Hq, G, HT;           // query heads, per kv head, head tiles per kv head
+  float scale_log2;
+};
+
+template <int C, bool FP8, int NT>
+struct Decode {
+  static constexpr int kRow = C * (FP8 ? 1 : 2);
+  static constexpr int kTile = kDecTile * kRow;
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kFit = 98304 / kStage;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kRows = 8 * NT;                 // heads of one item
+  static constexpr int kFrag = C / 4;                  // output values per lane and head tile
+  static constexpr int kOffX = kStages * kStage;       // three warps' outputs
+  static constexpr int kOffMl = kOffX + 3 * kFrag * 32 * 4;
+  static constexpr int kOffBar = kOffMl + 4 * kRows * 8;
+  static constexpr int kSmem = kOffBar + 256 + 1024;   // + alignment slack
+};
+
+// ------------------------------------------------------------ the linear order
+__device__ __forceinline__ int dec_tiles(const CacheView& c, int b) {
+  return (c.length(b) + kDecTile - 1) / kDecTile;
+}
+// sum of the tiles of all sequences (one warp)
+__device__ __forceinline__ long long dec_total(const CacheView& c, int lane) {
+  long long n = 0;
+  for (int b = lane; b < c.B; b += 32) n += dec_tiles(c, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// A place in the linear order: tile `tile` of `tiles` of head item `hk` of sequence b.
+struct DecPos {
+  int b, hk, tile, tiles;
+};
+// Place of linear tile t (0 <= t < total * per), `per` items per sequence (one warp).
+__device__ __forceinline__ DecPos dec_find(const CacheView& c, long long t, int per, int lane) {
+  long long base = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 32) {
+    const int n = b0 + lane < c.B ? dec_tiles(c, b0 + lane) : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, (base + incl) * per > t);
+    if (past != 0) {
+      const int l = __ffs(past) - 1;
+      const long long before = base + __shfl_sync(0xffffffffu, incl - n, l);
+      const int tiles = __shfl_sync(0xffffffffu, n, l);
+      const long long rem = t - before * per;
+      DecPos p;
+      p.b = b0 + l;
+      p.hk = (int)(rem / tiles);
+      p.tile = (int)(rem - (long long)p.hk * tiles);
+      p.tiles = tiles;
+      return p;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  DecPos none = {0, 0, 0, 1};
+  return none;
+}
+// the next item with a tile (there is one)
+__device__ __forceinline__ void dec_next_item(const CacheView& c, DecPos& p, int per) {
+  p.tile = 0;
+  if (++p.hk < per) return;
+  p.hk = 0;
+  do {
+    ++p.b;
+    p.tiles = p.b < c.B ? dec_tiles(c, p.b) : 1;
+  } while (p.tiles == 0);
+}
+
+// ------------------------------------------------------------ warp-level MMA
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two e4m3 (low half of x) -> f16x2, exact
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// rounded pair, and the pair of what the rounding left
+template <bool F16>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint32_t* lo) {
+  if (F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    *hi = *reinterpret_cast<const uint32_t*>(&h);
+    *lo = pack_f16x2(x - __low2float(h), y - __high2float(h));
+  } else {
+    *hi = pack_bf16x2(x, y);
+    *lo = pack_bf16x2(x - __uint_as_float(*hi << 16), y - __uint_as_float(*hi & 0xffff0000u));
+  }
+}
+__device__ __forceinline__ void bar_mma_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ------------------------------------------------------------------ split
+template <int C, bool FP8, int NT>
+__global__ void __launch_bounds__(kDecThreads, 2)
+decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ DecodeParams p) {
+  using L = Decode<C, FP8, NT>;
+  using namespace sm100;
+  constexpr int ST = L::kStages;
+  constexpr int kSteps = C / 16;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  float* xo = reinterpret_cast<float*>(smem + L::kOffX);        // [3][kFrag][32]
+  float2* xml = reinterpret_cast<float2*>(smem + L::kOffMl);    // [4][kRows]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* empty = full + ST;
+  uint32_t* parts = reinterpret_cast<uint32_t*>(empty + ST);    // [ST] page parts that were loaded
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(parts + ST);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = p.cache.Hkv * p.HT;
+
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // every warp finds the CTA's share for itself
+  const long long total = dec_total(p.cache, lane) * per;
+  const long long n_cta = total < gridDim.x ? total : gridDim.x;
+  if ((long long)blockIdx.x >= n_cta) return;
+  const long long t0 = blockIdx.x * total / n_cta;
+  const int mine = (int)((blockIdx.x + 1) * total / n_cta - t0);
+  DecPos at = dec_find(p.cache, t0, per, lane);
+  __syncthreads();
+
+  // a page holds a tile (or two), or a tile spans several pages
+  const int part_log2 = min(p.cache.page_log2, 6);     // keys of a page part
+  const int n_parts = kDecTile >> part_log2;
+
+  if (warp == 4) {
+    // ------------------------------------------------------ TMA producer
+    const uint32_t part_bytes = (uint32_t)L::kRow << part_log2;
+    if (lane == 0) {
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+    // lane l < n_parts looks up the page of part l, one tile ahead of its load
+    auto page_of = [&](const DecPos& q) -> int {
+      const int slot = q.tile * kDecTile + (lane << part_log2);
+      if (lane >= n_parts || slot >= p.cache.length(q.b)) return -1;
+      return __ldg(p.cache.page_table + (long long)q.b * p.cache.max_pages +
+                   (slot >> p.cache.page_log2));
+    };
+    auto advance = [&](DecPos& q) {
+      if (++q.tile == q.tiles) dec_next_item(p.cache, q, per);
+    };
+    int pid = page_of(at);
+    int n = 0;
+    for (; n < mine; ++n) {
+      const DecPos cur = at;
+      const int st = n % ST;
+      const int slot = cur.tile * kDecTile + (lane << part_log2);
+      const bool wanted = lane < n_parts && slot < p.cache.length(cur.b);
+      const bool good = wanted && pid >= 0 && pid < p.cache.num_pages;
+      const int row = (((pid * p.cache.Hkv) + cur.hk / p.HT) << p.cache.page_log2) +
+                      (slot & ((1 << p.cache.page_log2) - 1));
+      if (wanted && !good) raise_device_error(kErrInvalid);
+      int next_pid = -1;
+      if (n + 1 < mine) {
+        advance(at);
+        next_pid = page_of(at);
+      }
+      if (n >= ST &&
+          !__all_sync(0xffffffffu, mbar_wait(&empty[st], ((n / ST) - 1) & 1, abort_flag)))
+        break;
+      const unsigned loaded = __ballot_sync(0xffffffffu, good);
+      if (lane == 0) {
+        parts[st] = loaded;
+        mbar_expect_tx(&full[st], 2 * part_bytes * __popc(loaded));
+      }
+      __syncwarp();
+      if (good) {
+        const uint32_t dst = smem_u32(smem + st * L::kStage) + lane * part_bytes;
+        tma_load_3d(dst, &tmK, 0, row, 0, &full[st]);
+        tma_load_3d(dst + L::kTile, &tmV, 0, row, 0, &full[st]);
+      }
+      pid = next_pid;
+    }
+    // every load issued must land before the CTA may exit
+    volatile int no_abort = 0;
+    for (int i = (n > ST ? n - ST : 0); i < n; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, &no_abort);
+    return;
+  }
+
+  // ------------------------------------------------------------ MMA warps
+  const int k0 = warp * 16;                    // this warp's keys of a tile
+  const int hr = lane >> 2, i4 = lane & 3;     // MMA row (head), column group
+  const int part = k0 >> part_log2;
+  const uint32_t part_off = (uint32_t)part * ((uint32_t)L::kRow << part_log2);
+  const int r0 = k0 & ((1 << part_log2) - 1);  // first key's row inside its part
+  // shared address of 16-byte chunk `cb` of key row `r` (the TMA swizzle)
+  auto chunk = [&](uint32_t base, int r, int cb) -> uint32_t {
+    if (L::kRow == 64) return base + r * 64 + ((cb ^ ((r >> 1) & 3)) << 4);
+    const uint32_t half = (uint32_t)(cb >> 3) << (7 + part_log2);
+    return base + half + r * 128 + (((cb & 7) ^ (r & 7)) << 4);
+  };
+
+  bool ok = true;
+  int n = 0;
+  while (n < mine) {
+    const int len = p.cache.length(at.b);
+    const int kvh = at.hk / p.HT, ht = at.hk - kvh * p.HT;
+    const int h0 = kvh * p.G + ht * 16;                     // first query head of the item
+    const int heads = min(p.G - ht * 16, L::kRows);
+    const int seg_tiles = min(at.tiles - at.tile, mine - n);
+    const bool whole = seg_tiles == at.tiles;
+    const int item = at.b * per + at.hk;
+
+    // queries as the A operand: rows 0-7 heads 0-7, rows 8-15 heads 8-15 (NT = 2)
+    uint32_t qa[kSteps][2 * NT];
+    float mult[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int h = hr + 8 * t;
+      const bf16* q = p.q + (long long)at.b * p.q_sb + (long long)(h0 + h) * p.q_sh;
+      mult[t] = p.scale_log2;
+      if (!FP8) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          qa[s][t] = h < heads ? *reinterpret_cast<const uint32_t*>(q + s * 16 + i4 * 2) : 0u;
+          qa[s][NT + t] = h < heads ? *reinterpret_cast<const uint32_t*>(q + s * 16 + i4 * 2 + 8) : 0u;
+        }
+      } else {
+        // four neighbouring elements per lane and step: the order in which e4m3 pairs
+        // come out of a widened key row
+        uint2 raw[kSteps];
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          raw[s] = h < heads ? *reinterpret_cast<const uint2*>(q + s * 16 + i4 * 4) : make_uint2(0u, 0u);
+          const uint32_t w[2] = {raw[s].x, raw[s].y};
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            top = fmax3(top, fabsf(__uint_as_float(w[e] << 16)),
+                        fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e >= top; clamped so that 2^e and 2^-e are both normal
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 126, -126), 126);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          qa[s][t] = pack_f16x2(__uint_as_float(raw[s].x << 16) * down,
+                                __uint_as_float(raw[s].x & 0xffff0000u) * down);
+          qa[s][NT + t] = pack_f16x2(__uint_as_float(raw[s].y << 16) * down,
+                                     __uint_as_float(raw[s].y & 0xffff0000u) * down);
+        }
+        mult[t] = p.scale_log2 * __ldg(p.cache.k_scale + kvh) * __uint_as_float((uint32_t)(127 + e) << 23);
+      }
+    }
+
+    float m[NT], l[NT], o[NT][C / 8][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t] = kNegInf;
+      l[t] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C / 8; ++c) o[t][c][0] = o[t][c][1] = o[t][c][2] = o[t][c][3] = 0.f;
+    }
+
+    for (int s = 0; s < seg_tiles; ++s, ++n) {
+      const int st = n % ST;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (n / ST) & 1, abort_flag));
+      if (!ok) continue;
+      const int j0 = (at.tile + s) * kDecTile + k0;       // first slot of this warp's keys
+      const int live = ((parts[st] >> part) & 1) ? min(len - j0, 16) : 0;
+      if (live > 0) {
+        const uint32_t sK = smem_u32(smem + st * L::kStage) + part_off;
+        const uint32_t sV = sK + L::kTile;
+        if (live < 16) {     // stale rows behind the sequence's end: V = 0
+          constexpr int kCh = L::kRow / 16;
+          for (int i = lane; i < (16 - live) * kCh; i += 32) {
+            const uint32_t a = chunk(sV, r0 + live + i / kCh, i % kCh);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0) : "memory");
+          }
+          __syncwarp();
+        }
+        // S: rows heads, columns keys 0-7 and 8-15
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const int kr = r0 + ((lane >> 4) << 3) + (lane & 7);
+        if (!FP8) {
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t kb[4];
+            ldsm4(kb, chunk(sK, kr, 2 * k + ((lane >> 3) & 1)));
+            const uint32_t a[4] = {qa[k][0], NT == 2 ? qa[k][1] : 0u, qa[k][NT],
+                                   NT == 2 ? qa[k][2 * NT - 1] : 0u};
+            mma16816<false>(sc[0], a, kb[0], kb[1]);
+            mma16816<false>(sc[1], a, kb[2], kb[3]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            uint32_t kb[4];
+            ldsm4(kb, chunk(sK, kr, k + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t a[4] = {qa[k + u][0], NT == 2 ? qa[k + u][1] : 0u, qa[k + u][NT],
+                                     NT == 2 ? qa[k + u][2 * NT - 1] : 0u};
+              mma16816<true>(sc[0], a, e4m3x2_to_f16x2(kb[u]), e4m3x2_to_f16x2(kb[u] >> 16));
+              mma16816<true>(sc[1], a, e4m3x2_to_f16x2(kb[2 + u]), e4m3x2_to_f16x2(kb[2 + u] >> 16));
+            }
+          }
+        }
+        // softmax over this warp's 16 keys, base 2
+        uint32_t pa[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float x[4] = {sc[0][2 * t] * mult[t], sc[0][2 * t + 1] * mult[t], sc[1][2 * t] * mult[t],
+                        sc[1][2 * t + 1] * mult[t]};
+          if (live < 16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((e >> 1) * 8 + i4 * 2 + (e & 1) >= live) x[e] = kNegInf;
+          }
+          if (p.logits != nullptr && hr + 8 * t < heads) {
+            float* row = p.logits + ((long long)at.b * p.Hq + h0 + hr + 8 * t) * p.cache.capacity() +
+                         j0 + i4 * 2;
+            // a slot pair starts at an even slot, and the capacity is even
+            if (i4 * 2 < live) *reinterpret_cast<float2*>(row) = make_float2(x[0], x[1]);
+            if (8 + i4 * 2 < live) *reinterpret_cast<float2*>(row + 8) = make_float2(x[2], x[3]);
+          }
+          float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float m_new = fmaxf(m[t], mx);
+          if (__any_sync(0xffffffffu, m_new != m[t])) {
+            const float f = m_new == kNegInf ? 1.f : ex2(m[t] - m_new);
+            l[t] *= f;
+#pragma unroll
+            for (int c = 0; c < C / 8; ++c) {
+              o[t][c][0] *= f; o[t][c][1] *= f; o[t][c][2] *= f; o[t][c][3] *= f;
+            }
+            m[t] = m_new;
+          }
+          const float ref = m_new == kNegInf ? 0.f : m_new;
+          // one rounding between the logit and the exponential: the product again, fused
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = x[e] == kNegInf ? 0.f : ex2(fmaf(sc[e >> 1][2 * t + (e & 1)], mult[t], -ref));
+          l[t] += (x[0] + x[1]) + (x[2] + x[3]);
+          split_pair<FP8>(x[0], x[1], &pa[t][0], &pa[t][1]);
+          split_pair<FP8>(x[2], x[3], &pa[t][2], &pa[t][3]);
+        }
+        // O += P V
+        const int vr = r0 + (((lane >> 3) & 1) << 3) + (lane & 7);
+        if (!FP8) {
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t vb[4];
+            ldsm4t(vb, chunk(sV, vr, 2 * k + (lane >> 4)));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma16816<false>(o[t][2 * k], pa[t], vb[0], vb[1]);
+              mma16816<false>(o[t][2 * k + 1], pa[t], vb[2], vb[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            uint32_t vb[4];
+            ldsm4t(vb, chunk(sV, vr, k + (lane >> 4)));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              // a register holds columns (2n, 2n+1) of two keys: regroup by column
+              const uint32_t lo = __byte_perm(vb[2 * u], 0, 0x3120);
+              const uint32_t hi = __byte_perm(vb[2 * u + 1], 0, 0x3120);
+              const uint32_t e0 = e4m3x2_to_f16x2(lo), e1 = e4m3x2_to_f16x2(hi);
+              const uint32_t d0 = e4m3x2_to_f16x2(lo >> 16), d1 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                mma16816<true>(o[t][2 * (k + u)], pa[t], e0, e1);
+                mma16816<true>(o[t][2 * (k + u) + 1], pa[t], d0, d1);
+              }
+            }
+          }
+        }
+        // the zeroed rows were written through the generic proxy: order them before
+        // the next TMA write to this stage
+        if (live < 16) fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+
+    // ------------------------------------------- the four warps' outputs join
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
+      l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
+      if (i4 == 0) xml[warp * L::kRows + hr + 8 * t] = make_float2(m[t], l[t]);
+    }
+    bar_mma_warps();
+    const long long slot = (long long)blockIdx.x + item;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float top = kNegInf, sum = 0.f;
+      const int row = hr + 8 * t;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, xml[w * L::kRows + row].x);
+      const float ref = top == kNegInf ? 0.f : top;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 ml = xml[w * L::kRows + row];
+        sum += ex2(ml.x - ref) * ml.y;
+      }
+      const float f = ex2(m[t] - ref);
+      if (t > 0) bar_mma_warps();      // the previous head tile's values have been read
+      if (warp > 0) {
+#pragma unroll
+        for (int c = 0; c < C / 8; ++c) {
+          xo[((warp - 1) * L::kFrag + 2 * c) * 32 + lane] = (o[t][c][0] + o[t][c][2]) * f;
+          xo[((warp - 1) * L::kFrag + 2 * c + 1) * 32 + lane] = (o[t][c][1] + o[t][c][3]) * f;
+        }
+      }
+      bar_mma_warps();
+      if (warp == 0 && row < heads) {
+        const float vs = FP8 ? __ldg(p.cache.v_scale + kvh) : 1.f;
+        const float inv = whole ? vs / sum : vs;
+#pragma unroll
+        for (int c = 0; c < C / 8; c += 2) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int cc = c + (e >> 1), d = e & 1;
+            y[e] = (o[t][cc][d] + o[t][cc][d + 2]) * f;
+#pragma unroll
+            for (int w = 0; w < 3; ++w) y[e] += xo[(w * L::kFrag + 2 * cc + d) * 32 + lane];
+            y[e] = sum == 0.f ? 0.f : y[e] * inv;      // no mass: o = 0
+          }
+          // bf16: columns 8c + 2i, +1 and 8(c+1) + 2i, +1; e4m3: 8c + 4i .. +3, even and
+          // odd columns in neighbouring tiles
+          if (whole) {
+            bf16* out = p.O + ((long long)at.b * p.Hq + h0 + row) * C;
+            if (FP8) {
+              *reinterpret_cast<uint2*>(out + c * 8 + i4 * 4) =
+                  make_uint2(pack_bf16x2(y[0], y[2]), pack_bf16x2(y[1], y[3]));
+            } else {
+              *reinterpret_cast<uint32_t*>(out + c * 8 + i4 * 2) = pack_bf16x2(y[0], y[1]);
+              *reinterpret_cast<uint32_t*>(out + c * 8 + 8 + i4 * 2) = pack_bf16x2(y[2], y[3]);
+            }
+          } else {
+            float* out = p.part_o + (slot * L::kRows + row) * C;
+            if (FP8) {
+              *reinterpret_cast<float4*>(out + c * 8 + i4 * 4) = make_float4(y[0], y[2], y[1], y[3]);
+            } else {
+              *reinterpret_cast<float2*>(out + c * 8 + i4 * 2) = make_float2(y[0], y[1]);
+              *reinterpret_cast<float2*>(out + c * 8 + 8 + i4 * 2) = make_float2(y[2], y[3]);
+            }
+          }
+        }
+        if (i4 == 0) {
+          p.part_ml[slot * L::kRows + row] = make_float2(top, sum);
+          if (whole && p.lse != nullptr)
+            p.lse[(long long)at.b * p.Hq + h0 + row] =
+                sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
+        }
+      }
+    }
+    if (tid == 0) {
+      if (at.tile == 0) p.seg[item].x = blockIdx.x;
+      if (at.tile + seg_tiles == at.tiles) p.seg[item].y = blockIdx.x;
+    }
+    if (n < mine) dec_next_item(p.cache, at, per);
+  }
+}
+
+// ------------------------------------------------------------------- join
+// Blocks [0, B * Hq): output and lse of one query head from its partials. The others
+// (weights): acc_out[slot] = acc[slot] + sum over the group's heads of the slot's
+// softmax weight, from the logits of the split kernel and the joined statistics.
+template <int C>
+__global__ void __launch_bounds__(kJoinThreads)
+decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_per_tile,
+                   int weight_blocks) {
+  __shared__ float red[kJoinThreads];
+  __shared__ float stat[kDecMaxGroup];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int Hq = p.Hq, per = p.cache.Hkv * p.HT;
+  const int n_join = p.cache.B * Hq;
+
+  if ((int)blockIdx.x < n_join) {
+    const int b = blockIdx.x / Hq, h = blockIdx.x - b * Hq;
+    const int kvh = h / p.G, g = h - kvh * p.G;
+    bf16* out = p.O + (long long)blockIdx.x * C;
+    if (p.cache.length(b) == 0) {      // no key: o = 0, lse = -inf
+      if (tid < C) out[tid] = __float2bfloat16(0.f);
+      if (tid == 0) {
+        if (p.lse != nullptr) p.lse[blockIdx.x] = kNegInf;
+        if (!p.cache.length_valid(b)) raise_device_error(kErrInvalid);
+      }
+      return;
+    }
+    if (tid == 0 && !p.cache.length_valid(b)) raise_device_error(kErrInvalid);
+    const int item = b * per + kvh * p.HT + g / heads_per_tile;
+    const int row = g % heads_per_tile;
+    const int2 seg = p.seg[item];
+    if (seg.x == seg.y) return;        // one CTA had the whole item and finished it
+    const long long s0 = (long long)seg.x + item;
+    const int n = seg.y - seg.x + 1;
+    float top = kNegInf;
+    for (int s = 0; s < n; ++s) top = fmaxf(top, p.part_ml[(s0 + s) * rows + row].x);
+    const float ref = top == kNegInf ? 0.f : top;
+    constexpr int kGroups = kJoinThreads / C;
+    const int c = tid % C, gr = tid / C;
+    float sum = 0.f, y = 0.f;
+    for (int s = 0; s < n; ++s) {
+      const float2 ml = p.part_ml[(s0 + s) * rows + row];
+      sum += ex2(ml.x - ref) * ml.y;
+    }
+#pragma unroll 4
+    for (int s = gr; s < n; s += kGroups) {
+      const float f = ex2(p.part_ml[(s0 + s) * rows + row].x - ref);
+      y += f * p.part_o[((s0 + s) * rows + row) * C + c];
+    }
+    red[tid] = y;
+    __syncthreads();
+    if (gr == 0) {
+#pragma unroll
+      for (int k = 1; k < kGroups; ++k) y += red[k * C + c];
+      out[c] = __float2bfloat16(sum == 0.f ? 0.f : y / sum);
+      if (c == 0 && p.lse != nullptr)
+        p.lse[blockIdx.x] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- weights
+  const int wb = blockIdx.x - n_join;
+  const int pair = wb / weight_blocks, first = wb - pair * weight_blocks;
+  const int b = pair / p.cache.Hkv, kvh = pair - b * p.cache.Hkv;
+  const int len = p.cache.length(b);
+  if (first * kJoinThreads >= len) return;
+  // base-2 log-sum-exp of every head of the group
+  for (int g = warp; g < p.G; g += kJoinThreads / 32) {
+    const int item = b * per + kvh * p.HT + g / heads_per_tile;
+    const int row = g % heads_per_tile;
+    const int2 seg = p.seg[item];
+    const long long s0 = (long long)seg.x + item;
+    const int n = seg.y - seg.x + 1;
+    float top = kNegInf, sum = 0.f;
+    for (int s = lane; s < n; s += 32) top = fmaxf(top, p.part_ml[(s0 + s) * rows + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == kNegInf ? 0.f : top;
+    for (int s = lane; s < n; s += 32) {
+      const float2 ml = p.part_ml[(s0 + s) * rows + row];
+      sum += ex2(ml.x - ref) * ml.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // +inf: every weight of this head is 0 (it saw no mass)
+    if (lane == 0) stat[g] = sum == 0.f ? -kNegInf : ref + log2f(sum);
+  }
+  __syncthreads();
+  const float* logits = p.logits + ((long long)b * Hq + kvh * p.G) * p.cache.capacity();
+  for (int j = first * kJoinThreads + tid; j < len; j += weight_blocks * kJoinThreads) {
+    const long long at = p.cache.slot_index(b, kvh, j);
+    if (at < 0) continue;              // the split kernel raised the error
+    float w = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g) w += ex2(logits[(long long)g * p.cache.capacity() + j] - stat[g]);
+    p.acc_out[at] = p.cache.acc[at] + w;
+  }
+}
+
+}  // namespace xattn

@@ -346,7 +346,7 @@ const char* xattn_status_string(int status) {
   return "unknown status";
 }
 
-int xattn_version(void) { return 200; }
+int xattn_version(void) { return 201; }
 
 size_t xattn_score_workspace_size(int B, int Hq, int M, int stride, int block, int causal) {
   if (B < 0 || Hq < 0 || M < 0 || block != 128 || !stride_supported(stride) || M % block)
@@ -661,3 +661,5 @@ int xattn_get_device_error(void* stream) {
 }
 
 }  // extern "C"
+
+#include "cache_api.cuh"

@@ -73,7 +73,7 @@ typedef enum {
 XATTN_API const char* xattn_status_string(int status);
 
 /* Library ABI version (major*100 + minor); 200 since the workspace-size
- * functions take the causal flag. */
+ * functions take the causal flag, 201 with the decoding operators. */
 XATTN_API int xattn_version(void);
 
 /*
@@ -319,6 +319,171 @@ XATTN_API int xattn_sparse_attn_group(const void* Q, const void* K, const void* 
 XATTN_API int xattn_dense_attn(const void* Q, const void* K, const void* V,
                      int B, int Hq, int Hkv, int M, int C, int block, int causal,
                      float softmax_scale, void* O, float* lse, void* stream);
+
+/*
+ * ============================================================ after the prefill
+ * Decoding operators: rotary positions for Q and K, a paged key-value cache, the
+ * attention of one new token per sequence over it, and eviction from it. The pages
+ * describe the prefill only; these follow the common formulas stated here.
+ *
+ * Conventions beyond those above:
+ *   - Rows of bf16 heads are passed with their strides (xattn_heads), so that slices
+ *     of a fused projection need no copy. Elements of a row are contiguous; strides
+ *     count elements and are multiples of 8 (else XATTN_EUNSUPPORTED); rows are
+ *     16-byte aligned. An input may have a stride of 0; an output may not where that
+ *     would make two of its rows one (XATTN_EINVAL).
+ *   - The structs are read by the host during the call and may be reused at once.
+ *     Every pointer inside them is device memory, save that of the struct itself.
+ *   - lens, page_table, n_new, seen and pos are read on the device. A length outside
+ *     [0, max_pages * page], a page id outside [0, num_pages) that a length reaches,
+ *     or an n_new outside [0, min(T, lens)] touches no memory and raises
+ *     XATTN_EINVAL in the device error word; what such a sequence gets is
+ *     unspecified. Table entries behind a sequence's last page are never read as
+ *     pages and may hold anything.
+ *   - A page belongs to one (sequence, position in its table) for every call that
+ *     writes to it (append, evict, and decoding with acc_out). Decoding without
+ *     acc_out may share pages between sequences.
+ *   - A workspace serves one call at a time: calls that may overlap on the GPU (two
+ *     streams, two captured graphs) need one each.
+ *   - C in {64, 128}; page in {16, 32, 64, 128}; B * Hkv <= 65535.
+ */
+
+/* bf16 rows [B, heads, M, C] at element strides; C is contiguous. */
+typedef struct {
+  void* data;
+  long long stride_b, stride_h, stride_m;
+  int heads;
+} xattn_heads;
+
+#define XATTN_ROPE_MAX_AXES 4
+
+/*
+ * Rotary positions. A row has pairs = sections[0] + ... + sections[axes-1] rotated
+ * pairs (a multiple of 8, at most C/2); the first sections[0] of them turn by the
+ * token's position on axis 0, the next sections[1] by that on axis 1, and so on
+ * (text: one axis; video: time, height, width). Pair p is the elements (p, p + pairs),
+ * or (2p, 2p + 1) if interleaved; elements behind 2 * pairs pass through.
+ *   pos       int32 [pos_batch, M, axes], pos_batch = 1 (shared) or B
+ *   inv_freq  fp64 [pairs]: pair p turns by pos[axis(p)] * inv_freq[p] radians
+ */
+typedef struct {
+  const int32_t* pos;
+  const double* inv_freq;
+  int sections[XATTN_ROPE_MAX_AXES];
+  int axes, interleaved, pos_batch;
+} xattn_rotary;
+
+/*
+ * xattn_rope - (x1, x2) -> (x1 cos a - x2 sin a, x2 cos a + x1 sin a) for every pair of
+ * every row of Q and K; inverse != 0 turns by -a, which undoes the rotation and is
+ * also its gradient. Angles are formed in 64 bits, the rotation in 32, rounded once.
+ *   Q, K    inputs; K and Ko may both be NULL
+ *   Qo, Ko  outputs, with their own strides; an output may be its input itself (same
+ *           pointer and strides), and may not overlap it in any other way
+ * For the prefill, give Qo and Ko as dense [B, H, M, C].
+ */
+XATTN_API int xattn_rope(const xattn_heads* Q, const xattn_heads* K, const xattn_rotary* rot,
+                         int inverse, int B, int M, int C, const xattn_heads* Qo,
+                         const xattn_heads* Ko, void* stream);
+
+/* Element types of the cache's pages. */
+typedef enum {
+  XATTN_KV_BF16 = 0,
+  XATTN_KV_E4M3 = 1   /* a stored x stands for x * k_scale[h] (v_scale[h]), scales > 0 */
+} xattn_kv_type;
+
+/*
+ * A paged cache of B sequences. Slot s of sequence b lies in page
+ * page_table[b * max_pages + s / page], row s % page of it. All layers of a model can
+ * share one page_table and one lens.
+ *   k_pages, v_pages   [num_pages, Hkv, page, C] in kv_type, 16-byte aligned
+ *   k_scale, v_scale   fp32 [Hkv] (e4m3 only)
+ *   acc                fp32 [num_pages, Hkv, page], accumulated attention weight of each
+ *                      slot, or NULL
+ *   ordinal            int32 [num_pages, Hkv, page], index of the slot's token in its
+ *                      sequence, or NULL
+ *   page_table         int32 [B, max_pages];  lens  int32 [B], slots in use
+ */
+typedef struct {
+  void *k_pages, *v_pages;
+  const float *k_scale, *v_scale;
+  float* acc;
+  int32_t* ordinal;
+  const int32_t* page_table;
+  const int32_t* lens;
+  int B, Hkv, C, page, num_pages, max_pages, kv_type;
+} xattn_cache;
+
+/*
+ * xattn_cache_append - the last n_new[b] slots of every sequence from K and V
+ * [B, Hkv, T, C]: token t < n_new[b] goes to slot lens[b] - n_new[b] + t. lens already
+ * counts the new tokens (advance it once per step, for all layers). Tokens t >=
+ * n_new[b] are padding and are not read. acc of the new slots becomes 0, their ordinal
+ * seen[b] - n_new[b] + t (each if present).
+ *   n_new  int32 [B], or NULL for T new tokens everywhere
+ *   seen   int32 [B], tokens of the sequence so far including the new ones (more than
+ *          lens once tokens were evicted), or NULL for lens
+ * e4m3 pages take x / scale, rounded once to nearest and saturated at +-448.
+ */
+XATTN_API int xattn_cache_append(const xattn_heads* K, const xattn_heads* V,
+                                 const xattn_cache* cache, int T, const int32_t* n_new,
+                                 const int32_t* seen, void* stream);
+
+/*
+ * xattn_rope_append - xattn_rope of Q and K and xattn_cache_append of the rotated K and
+ * of V, in one launch: the decoding step's first. Qo gets the rotated queries of the
+ * tokens t < n_new[b]; its other rows are left as they were. K goes from fp32 straight
+ * to the page's type.
+ */
+XATTN_API int xattn_rope_append(const xattn_heads* Q, const xattn_heads* K, const xattn_heads* V,
+                                const xattn_rotary* rot, const xattn_cache* cache, int T,
+                                const int32_t* n_new, const int32_t* seen, const xattn_heads* Qo,
+                                void* stream);
+
+/* Workspace bytes of xattn_decode_attn for Hq query heads; weights != 0 if acc_out is
+ * given. It depends on the cache's shape, not on the lengths. 0 for bad arguments. */
+XATTN_API size_t xattn_decode_workspace_size(const xattn_cache* cache, int Hq, int weights);
+
+/*
+ * xattn_decode_attn - softmax attention of one query per sequence and head over the
+ * slots s < lens[b]:
+ *   O[b,h] = sum_s p_s v_s,  p = softmax(softmax_scale * q_h . k_s),
+ * with K and V of head h / (Hq/Hkv). A sequence of length 0 gets O = 0, lse = -inf.
+ *   Q        [B, Hq, 1, C] at its strides (stride_m is not used); Hq/Hkv <= 128
+ *   O        bf16 [B, Hq, C], dense
+ *   lse      fp32 [B, Hq], natural-log log-sum-exp, or NULL
+ *   acc_out  fp32 [num_pages, Hkv, page] or NULL: acc_out = acc + sum of p over the query
+ *            heads of the slot's kv head, for the slots in use (the others are left as
+ *            they were). May be cache->acc itself, and must not overlap it otherwise.
+ *   workspace  device buffer, 16-byte aligned; contents on entry are ignored
+ * The sums and the softmax are fp32; results do not depend on the order in which the
+ * GPU runs its blocks.
+ */
+XATTN_API int xattn_decode_attn(const xattn_heads* Q, const xattn_cache* cache,
+                                float softmax_scale, void* O, float* lse, float* acc_out,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of xattn_cache_evict; 0 for bad arguments. */
+XATTN_API size_t xattn_cache_evict_workspace_size(const xattn_cache* cache, int budget);
+
+/*
+ * xattn_cache_evict - keeps n = min(lens[b], budget) slots of every sequence and kv head,
+ * in slots 0..n-1. Kept are first the safe slots (ordinal >= seen[b] - recent, or
+ * ordinal < sink), then those of the largest acc; equal ones by slot, ascending. NaN
+ * counts as larger than +inf. A kept slot below n stays in place; the i-th evicted slot
+ * below n (ascending) takes the row, acc and ordinal of the i-th kept slot from the end.
+ * The order of slots carries no meaning for xattn_decode_attn; ordinals tell the tokens.
+ * lens is not changed, because layers may share it: clamp it to budget after the last
+ * layer. Slots from n on are left as they were.
+ *   budget   >= 1;  recent, sink >= 0, recent + sink <= budget
+ *   seen     int32 [B], as in xattn_cache_append, or NULL for lens
+ *   acc_out, ord_out  like acc and ordinal; slots 0..n-1 are written. Each may be
+ *            the cache's own array (in place), and must not overlap it otherwise.
+ * cache->acc and cache->ordinal must be present.
+ */
+XATTN_API int xattn_cache_evict(const xattn_cache* cache, int budget, int recent, int sink,
+                                const int32_t* seen, float* acc_out, int32_t* ord_out,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * xattn_selftest_wait_timeout - diagnostic of the bounded device waits (the
