@@ -116,7 +116,10 @@ class _Lazy:
     def __getattr__(self, name):
         if _Lazy._cdll is None:
             _Lazy._cdll = _load()
-        return getattr(_Lazy._cdll, name)
+        fn = getattr(_Lazy._cdll, name)
+        if name in SIGNATURES:
+            setattr(self, name, fn)     # the next call finds it without coming here
+        return fn
 
 
 _lib = _Lazy()
@@ -391,52 +394,55 @@ def xattn_prefill(Q, K, V, tau, stride: int, causal: bool, bufs: Buffers,
 
 
 # ----------------------------------------------------- decoding operators
-def _device_of(*ts):
-    """The one device of the given tensors (None entries aside)."""
-    dev = None
+def _device_of(*ts) -> int:
+    """Index of the one device of the given tensors (None entries aside)."""
+    dev = -2
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors are on different devices ({dev} and {t.device})")
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if i < 0:
+                    raise ValueError("tensors must be CUDA tensors")
+                if dev >= 0:
+                    raise ValueError(f"tensors are on different devices (cuda:{dev} and cuda:{i})")
+                dev = i
     return dev
 
 
-def _call(name: str, dev, stream, *args) -> None:
-    """Calls a C entry point on `stream` (default: the current one of `dev`), with `dev`
-    the current device."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            rc = getattr(_lib, name)(*args, _stream(stream))
+def _call(fn, dev: int, stream, *args) -> None:
+    """Calls a C entry point on `stream` (default: the current one of device `dev`), with
+    `dev` the current device. A decoding step is a few microseconds of GPU time, so this
+    path avoids the objects that torch.cuda.current_stream() and .device would make."""
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, st)
     else:
-        rc = getattr(_lib, name)(*args, _stream(stream))
+        with torch.cuda.device(dev):
+            rc = fn(*args, st)
     if rc != XATTN_OK:
-        raise XAttnError(rc, name)
+        raise XAttnError(rc, fn.__name__)
 
 
 def _heads(t: torch.Tensor, what: str, shape=None) -> _Heads:
     """[B, H, M, C] bf16 rows at any strides with contiguous elements."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{what} must be bfloat16")
-    if t.dim() != 4 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}" +
-                         (f", {tuple(shape)} is wanted" if shape is not None else ", [B, H, M, C] is wanted"))
+    size = t.shape
+    if size != shape and (shape is not None or len(size) != 4):
+        raise ValueError(f"{what} has shape {tuple(size)}, "
+                         f"{'[B, H, M, C]' if shape is None else tuple(shape)} is wanted")
+    B, H, M, C = size
     sb, sh, sm, sc = t.stride()
-    if sc != 1 and t.shape[3] > 1:
+    if sc != 1 and C > 1:
         raise ValueError(f"the elements of a row of {what} must be contiguous")
-    B, H, M, _ = t.shape
     # the stride of a dimension of size 1 means nothing and need not be aligned
     return _Heads(t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, sm if M > 1 else 0, H)
 
 
 def _want(t, what: str, dtype, shape) -> None:
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} is wanted")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
@@ -483,7 +489,8 @@ class PagedCache:
     page_table        int32 [B, max_pages];  lens  int32 [B], slots in use
     k_scale, v_scale  fp32 [Hkv], for float8_e4m3fn pages
     acc, ordinal      fp32 / int32 [num_pages, Hkv, page], for eviction
-    The tensors are the caller's; the cache holds references and checks them once.
+    The tensors are the caller's; the cache holds references and checks them once, so its
+    attributes cannot be replaced (make a new PagedCache), only written into.
     """
 
     def __init__(self, k_pages, v_pages, page_table, lens, k_scale=None, v_scale=None, acc=None,
@@ -508,12 +515,21 @@ class PagedCache:
             _want(acc, "acc", torch.float32, (P, Hkv, page))
         if ordinal is not None:
             _want(ordinal, "ordinal", torch.int32, (P, Hkv, page))
-        self.device = _device_of(k_pages, v_pages, page_table, lens, k_scale, v_scale, acc, ordinal)
+        _device_of(k_pages, v_pages, page_table, lens, k_scale, v_scale, acc, ordinal)
         self.k_pages, self.v_pages, self.page_table, self.lens = k_pages, v_pages, page_table, lens
         self.k_scale, self.v_scale, self.acc, self.ordinal = k_scale, v_scale, acc, ordinal
         self.B, self.Hkv, self.C, self.page = B, Hkv, C, page
         self.num_pages, self.max_pages = P, max_pages
         self.kv_type = XATTN_KV_E4M3 if e4m3 else XATTN_KV_BF16
+        self._c = _Cache(B=B, Hkv=Hkv, C=C, page=page, num_pages=P, max_pages=max_pages,
+                         kv_type=self.kv_type)
+        self._checked = True
+
+    def __setattr__(self, name, value):
+        # cache.lens += 1 works in place and assigns the same tensor
+        if "_checked" in self.__dict__ and self.__dict__.get(name) is not value:
+            raise AttributeError(f"{name}: the tensors of a PagedCache are fixed")
+        self.__dict__[name] = value
 
     @staticmethod
     def allocate(B, Hkv, C, num_pages, max_pages, page=64, dtype=torch.bfloat16, eviction=False,
@@ -535,10 +551,13 @@ class PagedCache:
             torch.zeros(pool, dtype=torch.int32, device=dev) if eviction else None)
 
     def _struct(self) -> _Cache:
-        return _Cache(self.k_pages.data_ptr(), self.v_pages.data_ptr(), _ptr(self.k_scale),
-                      _ptr(self.v_scale), _ptr(self.acc), _ptr(self.ordinal),
-                      self.page_table.data_ptr(), self.lens.data_ptr(), self.B, self.Hkv, self.C,
-                      self.page, self.num_pages, self.max_pages, self.kv_type)
+        # the shapes are fixed; the addresses are read on every call
+        c = self._c
+        c.k_pages, c.v_pages = self.k_pages.data_ptr(), self.v_pages.data_ptr()
+        c.k_scale, c.v_scale = _ptr(self.k_scale), _ptr(self.v_scale)
+        c.acc, c.ordinal = _ptr(self.acc), _ptr(self.ordinal)
+        c.page_table, c.lens = self.page_table.data_ptr(), self.lens.data_ptr()
+        return c
 
 
 def xattn_rope(Q, K, pos, rotary: Rotary, Qo, Ko, inverse: bool = False, stream=None) -> None:
@@ -554,7 +573,7 @@ def xattn_rope(Q, K, pos, rotary: Rotary, Qo, Ko, inverse: bool = False, stream=
     k = ko = None
     if K is not None:
         k, ko = _heads(K, "K", (B, K.shape[1], M, C)), _heads(Ko, "Ko", K.shape)
-    _call("xattn_rope", dev, stream, q, k, rotary._struct(pos, B, M), int(inverse), B, M, C, qo, ko)
+    _call(_lib.xattn_rope, dev, stream, q, k, rotary._struct(pos, B, M), int(inverse), B, M, C, qo, ko)
 
 
 def _per_sequence(t, what: str, B: int):
@@ -569,7 +588,7 @@ def xattn_cache_append(K, V, cache: PagedCache, n_new=None, seen=None, stream=No
     of the sequence, evicted ones too."""
     dev = _device_of(K, V, cache.k_pages, n_new, seen)
     shape = (cache.B, cache.Hkv, K.shape[2], cache.C)
-    _call("xattn_cache_append", dev, stream, _heads(K, "K", shape), _heads(V, "V", shape),
+    _call(_lib.xattn_cache_append, dev, stream, _heads(K, "K", shape), _heads(V, "V", shape),
           cache._struct(), shape[2], _per_sequence(n_new, "n_new", cache.B),
           _per_sequence(seen, "seen", cache.B))
 
@@ -581,7 +600,7 @@ def xattn_rope_append(Q, K, V, pos, rotary: Rotary, cache: PagedCache, Qo, n_new
     dev = _device_of(Q, K, V, pos, rotary.inv_freq, cache.k_pages, Qo, n_new, seen)
     B, T = cache.B, K.shape[2]
     shape = (B, cache.Hkv, T, cache.C)
-    _call("xattn_rope_append", dev, stream, _heads(Q, "Q", (B, Q.shape[1], T, cache.C)),
+    _call(_lib.xattn_rope_append, dev, stream, _heads(Q, "Q", (B, Q.shape[1], T, cache.C)),
           _heads(K, "K", shape), _heads(V, "V", shape), rotary._struct(pos, B, T), cache._struct(), T,
           _per_sequence(n_new, "n_new", B), _per_sequence(seen, "seen", B),
           _heads(Qo, "Qo", Q.shape))
@@ -613,7 +632,7 @@ def xattn_decode_attn(Q, cache: PagedCache, softmax_scale: float, O, workspace, 
     elif acc_out is not None:
         raise ValueError("acc_out needs weights=True")
     _want(workspace, "workspace", workspace.dtype, workspace.shape)
-    _call("xattn_decode_attn", dev, stream, q, cache._struct(), float(softmax_scale), O.data_ptr(),
+    _call(_lib.xattn_decode_attn, dev, stream, q, cache._struct(), float(softmax_scale), O.data_ptr(),
           _ptr(lse), _ptr(acc_out), workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
 
@@ -640,6 +659,6 @@ def xattn_cache_evict(cache: PagedCache, budget: int, workspace, recent: int = 0
     else:
         _want(ord_out, "ord_out", torch.int32, cache.ordinal.shape)
     _want(workspace, "workspace", workspace.dtype, workspace.shape)
-    _call("xattn_cache_evict", dev, stream, cache._struct(), int(budget), int(recent), int(sink),
+    _call(_lib.xattn_cache_evict, dev, stream, cache._struct(), int(budget), int(recent), int(sink),
           _per_sequence(seen, "seen", cache.B), acc_out.data_ptr(), ord_out.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())

@@ -14,6 +14,23 @@ inline int ilog2(int v) {
   return n;
 }
 
+// Launches `kern` so that it may start before the kernel ahead of it in the stream has
+// ended; it must begin with grid_dependency_wait().
+template <typename... P, typename... A>
+int launch_dependent(void (*kern)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return XATTN_ECUDA;
+  return launch_status();
+}
+
 bool page_supported(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 
 // What every entry point asks of a cache. *empty: nothing to do (B or Hkv is 0).
@@ -257,12 +274,13 @@ int launch_decode(const xattn_cache* c, DecodeParams& p, const DecodePlan& d, cu
   long long wb = 0;
   if (p.acc_out != nullptr) {
     const long long pairs = (long long)c->B * c->Hkv;
-    wb = std::min<long long>(((long long)c->max_pages * c->page + kJoinThreads - 1) / kJoinThreads,
+    constexpr int kSlots = 4 * kJoinThreads;     // slots of a block's sweep
+    wb = std::min<long long>(((long long)c->max_pages * c->page + kSlots - 1) / kSlots,
                              std::max<long long>(1, 148 * 4 / pairs));
   }
   const long long blocks = (long long)c->B * p.Hq + wb * c->B * c->Hkv;
-  decode_join_kernel<C><<<(unsigned)blocks, kJoinThreads, 0, st>>>(p, d.rows, 8 * d.NT, (int)wb);
-  return launch_status();
+  return launch_dependent(decode_join_kernel<C>, dim3((unsigned)blocks), kJoinThreads, st, p, d.rows,
+                          8 * d.NT, (int)wb);
 }
 
 // ------------------------------------------------------------------ evict
@@ -426,12 +444,11 @@ int xattn_cache_evict(const xattn_cache* cache, int budget, int recent, int sink
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return XATTN_ECUDA;
   if (e.max_moves == 0) return launch_status();
-  const int per_block = kEvMoveThreads * 4 * 16 / (2 << p.row_bytes_log2);   // moves of one sweep
+  const int per_block = kEvMoveThreads * kEvMoveUnroll >> (p.row_bytes_log2 - 4);   // moves of a sweep
   const long long most = (e.max_moves + per_block - 1) / per_block;
   const long long fill = std::max<long long>(1, 148 * 8 / e.rows);
-  evict_move_kernel<<<dim3((unsigned)std::min(most, fill), (unsigned)e.rows), kEvMoveThreads, 0,
-                      st>>>(p);
-  return launch_status();
+  return launch_dependent(evict_move_kernel, dim3((unsigned)std::min(most, fill), (unsigned)e.rows),
+                          kEvMoveThreads, st, p);
 }
 
 }  // extern "C"

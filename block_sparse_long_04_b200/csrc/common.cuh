@@ -42,6 +42,16 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+// Programmatic dependent launch: a kernel launched with that attribute may start while
+// the kernel before it in the stream still runs, and waits here until that one has
+// completed and its writes are visible; the earlier kernel allows the start.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependents_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // max of three fp32 values in one instruction (sm_100)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;

@@ -6,7 +6,7 @@
 // sets the pace (4 to 16 flops per byte at the usual group sizes). The kernel's task is
 // to keep enough bytes in flight on every SM and to stay off everybody's critical path.
 //
-// Split. The tiles (64 keys) of all (sequence, kv head) items form one linear order,
+// Split. The tiles (64 or 128 keys) of all (sequence, kv head) items form one linear order,
 // which is cut into equal shares, one per CTA: ragged batches and single long sequences
 // load all SMs alike, and nothing has to be planned on the host. A CTA walks its share;
 // where an item ends inside it, the partial (maximum, sum, unnormalised output) goes to
@@ -15,7 +15,7 @@
 // order c + i grows, so c + i numbers the partials.
 //
 // One CTA (two per SM): warp 4 loads K and V tiles by TMA, one box per page part, into
-// a ring of stages; warps 0-3 own 16 of the tile's 64 keys each and run
+// a ring of stages; warps 0-3 own a quarter of the tile's keys each and run
 // independently (own maximum, sum and output) until the item's end. The products use
 // warp-level MMAs: with Hq/Hkv <= 16 query rows the tensor work is a few percent of what
 // even that path offers, while a tcgen05 tile (M = 128) would hold 8 to 32 useful rows
@@ -39,7 +39,6 @@
 
 namespace xattn {
 
-constexpr int kDecTile = 64;          // keys per stage
 constexpr int kDecThreads = 160;      // four MMA warps, one TMA warp
 constexpr int kDecCtas = 296;         // 148 SMs x 2
 constexpr int kJoinThreads = 512;
@@ -60,10 +59,20 @@ struct DecodeParams {
   float scale_log2;
 };
 
+// Keys per tile: 64, or 128 where that fits a 32 KB stage and the registers: a warp
+// then works on two independent sets of 16 keys, which hides the latencies of its chain
+// (load, widen, product, maximum, exponential, product) and halves its overhead per key.
+// Ragged e4m3 batch of 32 (0.54 GB): 64 keys 128 us, 128 keys see below.
+__host__ __device__ constexpr int dec_tile_keys(int C, bool fp8, int NT) {
+  return NT == 1 && C * (fp8 ? 1 : 2) <= 128 ? 128 : 64;
+}
+
 template <int C, bool FP8, int NT>
 struct Decode {
   static constexpr int kRow = C * (FP8 ? 1 : 2);
-  static constexpr int kTile = kDecTile * kRow;
+  static constexpr int kKeys = dec_tile_keys(C, FP8, NT);
+  static constexpr int kSets = kKeys / 64;             // sets of 16 keys per warp
+  static constexpr int kTile = kKeys * kRow;
   static constexpr int kStage = 2 * kTile;
   static constexpr int kFit = 98304 / kStage;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -76,13 +85,15 @@ struct Decode {
 };
 
 // ------------------------------------------------------------ the linear order
+template <int KEYS>
 __device__ __forceinline__ int dec_tiles(const CacheView& c, int b) {
-  return (c.length(b) + kDecTile - 1) / kDecTile;
+  return (c.length(b) + KEYS - 1) / KEYS;
 }
 // sum of the tiles of all sequences (one warp)
+template <int KEYS>
 __device__ __forceinline__ long long dec_total(const CacheView& c, int lane) {
   long long n = 0;
-  for (int b = lane; b < c.B; b += 32) n += dec_tiles(c, b);
+  for (int b = lane; b < c.B; b += 32) n += dec_tiles<KEYS>(c, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n;
@@ -93,10 +104,11 @@ struct DecPos {
   int b, hk, tile, tiles;
 };
 // Place of linear tile t (0 <= t < total * per), `per` items per sequence (one warp).
+template <int KEYS>
 __device__ __forceinline__ DecPos dec_find(const CacheView& c, long long t, int per, int lane) {
   long long base = 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const int n = b0 + lane < c.B ? dec_tiles(c, b0 + lane) : 0;
+    const int n = b0 + lane < c.B ? dec_tiles<KEYS>(c, b0 + lane) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -122,13 +134,14 @@ __device__ __forceinline__ DecPos dec_find(const CacheView& c, long long t, int 
   return none;
 }
 // the next item with a tile (there is one)
+template <int KEYS>
 __device__ __forceinline__ void dec_next_item(const CacheView& c, DecPos& p, int per) {
   p.tile = 0;
   if (++p.hk < per) return;
   p.hk = 0;
   do {
     ++p.b;
-    p.tiles = p.b < c.B ? dec_tiles(c, p.b) : 1;
+    p.tiles = p.b < c.B ? dec_tiles<KEYS>(c, p.b) : 1;
   } while (p.tiles == 0);
 }
 
@@ -210,6 +223,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = p.cache.Hkv * p.HT;
+  grid_dependents_may_start();     // the join's blocks wait for this grid's end themselves
 
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -220,17 +234,17 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
     fence_mbar_init();
   }
   // every warp finds the CTA's share for itself
-  const long long total = dec_total(p.cache, lane) * per;
+  const long long total = dec_total<L::kKeys>(p.cache, lane) * per;
   const long long n_cta = total < gridDim.x ? total : gridDim.x;
   if ((long long)blockIdx.x >= n_cta) return;
   const long long t0 = blockIdx.x * total / n_cta;
   const int mine = (int)((blockIdx.x + 1) * total / n_cta - t0);
-  DecPos at = dec_find(p.cache, t0, per, lane);
+  DecPos at = dec_find<L::kKeys>(p.cache, t0, per, lane);
   __syncthreads();
 
   // a page holds a tile (or two), or a tile spans several pages
-  const int part_log2 = min(p.cache.page_log2, 6);     // keys of a page part
-  const int n_parts = kDecTile >> part_log2;
+  const int part_log2 = min(p.cache.page_log2, 6);     // keys of a page part (one TMA box)
+  const int n_parts = L::kKeys >> part_log2;
 
   if (warp == 4) {
     // ------------------------------------------------------ TMA producer
@@ -241,20 +255,20 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
     }
     // lane l < n_parts looks up the page of part l, one tile ahead of its load
     auto page_of = [&](const DecPos& q) -> int {
-      const int slot = q.tile * kDecTile + (lane << part_log2);
+      const int slot = q.tile * L::kKeys + (lane << part_log2);
       if (lane >= n_parts || slot >= p.cache.length(q.b)) return -1;
       return __ldg(p.cache.page_table + (long long)q.b * p.cache.max_pages +
                    (slot >> p.cache.page_log2));
     };
     auto advance = [&](DecPos& q) {
-      if (++q.tile == q.tiles) dec_next_item(p.cache, q, per);
+      if (++q.tile == q.tiles) dec_next_item<L::kKeys>(p.cache, q, per);
     };
     int pid = page_of(at);
     int n = 0;
     for (; n < mine; ++n) {
       const DecPos cur = at;
       const int st = n % ST;
-      const int slot = cur.tile * kDecTile + (lane << part_log2);
+      const int slot = cur.tile * L::kKeys + (lane << part_log2);
       const bool wanted = lane < n_parts && slot < p.cache.length(cur.b);
       const bool good = wanted && pid >= 0 && pid < p.cache.num_pages;
       const int row = (((pid * p.cache.Hkv) + cur.hk / p.HT) << p.cache.page_log2) +
@@ -288,11 +302,19 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
   }
 
   // ------------------------------------------------------------ MMA warps
-  const int k0 = warp * 16;                    // this warp's keys of a tile
+  constexpr int SETS = L::kSets;
   const int hr = lane >> 2, i4 = lane & 3;     // MMA row (head), column group
-  const int part = k0 >> part_log2;
-  const uint32_t part_off = (uint32_t)part * ((uint32_t)L::kRow << part_log2);
-  const int r0 = k0 & ((1 << part_log2) - 1);  // first key's row inside its part
+  // this warp's sets of 16 keys: first key in the tile, page part, and place of the part's
+  // rows in a stage
+  int k0[SETS], part[SETS], r0[SETS];
+  uint32_t part_off[SETS];
+#pragma unroll
+  for (int u = 0; u < SETS; ++u) {
+    k0[u] = (warp * SETS + u) * 16;
+    part[u] = k0[u] >> part_log2;
+    r0[u] = k0[u] & ((1 << part_log2) - 1);
+    part_off[u] = (uint32_t)part[u] * ((uint32_t)L::kRow << part_log2);
+  }
   // shared address of 16-byte chunk `cb` of key row `r` (the TMA swizzle)
   auto chunk = [&](uint32_t base, int r, int cb) -> uint32_t {
     if (L::kRow == 64) return base + r * 64 + ((cb ^ ((r >> 1) & 3)) << 4);
@@ -368,122 +390,152 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
       const int st = n % ST;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (n / ST) & 1, abort_flag));
       if (!ok) continue;
-      const int j0 = (at.tile + s) * kDecTile + k0;       // first slot of this warp's keys
-      const int live = ((parts[st] >> part) & 1) ? min(len - j0, 16) : 0;
-      if (live > 0) {
-        const uint32_t sK = smem_u32(smem + st * L::kStage) + part_off;
-        const uint32_t sV = sK + L::kTile;
-        if (live < 16) {     // stale rows behind the sequence's end: V = 0
+      const int t_first = (at.tile + s) * L::kKeys;
+      const uint32_t loaded = parts[st];
+      int live[SETS], most = 0, least = 16;        // keys of a set that exist
+#pragma unroll
+      for (int u = 0; u < SETS; ++u) {
+        live[u] = ((loaded >> part[u]) & 1) ? max(min(len - t_first - k0[u], 16), 0) : 0;
+        most = max(most, live[u]);
+        least = min(least, live[u]);
+      }
+      if (most > 0) {
+        const uint32_t stage = smem_u32(smem + st * L::kStage);
+        if (least < 16) {     // stale rows behind the sequence's end: V = 0
           constexpr int kCh = L::kRow / 16;
-          for (int i = lane; i < (16 - live) * kCh; i += 32) {
-            const uint32_t a = chunk(sV, r0 + live + i / kCh, i % kCh);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0) : "memory");
-          }
+#pragma unroll
+          for (int u = 0; u < SETS; ++u)
+            for (int i = lane; i < (16 - live[u]) * kCh; i += 32) {
+              const uint32_t a = chunk(stage + L::kTile + part_off[u], r0[u] + live[u] + i / kCh, i % kCh);
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0) : "memory");
+            }
           __syncwarp();
         }
-        // S: rows heads, columns keys 0-7 and 8-15
-        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const int kr = r0 + ((lane >> 4) << 3) + (lane & 7);
+        // S: rows heads, columns keys 0-7 and 8-15 of each set
+        float sc[SETS][2][4];
+#pragma unroll
+        for (int u = 0; u < SETS; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[u][0][e] = sc[u][1][e] = 0.f;
+        const int kr = ((lane >> 4) << 3) + (lane & 7);
         if (!FP8) {
 #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
-            uint32_t kb[4];
-            ldsm4(kb, chunk(sK, kr, 2 * k + ((lane >> 3) & 1)));
             const uint32_t a[4] = {qa[k][0], NT == 2 ? qa[k][1] : 0u, qa[k][NT],
                                    NT == 2 ? qa[k][2 * NT - 1] : 0u};
-            mma16816<false>(sc[0], a, kb[0], kb[1]);
-            mma16816<false>(sc[1], a, kb[2], kb[3]);
+#pragma unroll
+            for (int u = 0; u < SETS; ++u) {
+              uint32_t kb[4];
+              ldsm4(kb, chunk(stage + part_off[u], r0[u] + kr, 2 * k + ((lane >> 3) & 1)));
+              mma16816<false>(sc[u][0], a, kb[0], kb[1]);
+              mma16816<false>(sc[u][1], a, kb[2], kb[3]);
+            }
           }
         } else {
 #pragma unroll
           for (int k = 0; k < kSteps; k += 2) {
-            uint32_t kb[4];
-            ldsm4(kb, chunk(sK, kr, k + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t a[4] = {qa[k + u][0], NT == 2 ? qa[k + u][1] : 0u, qa[k + u][NT],
-                                     NT == 2 ? qa[k + u][2 * NT - 1] : 0u};
-              mma16816<true>(sc[0], a, e4m3x2_to_f16x2(kb[u]), e4m3x2_to_f16x2(kb[u] >> 16));
-              mma16816<true>(sc[1], a, e4m3x2_to_f16x2(kb[2 + u]), e4m3x2_to_f16x2(kb[2 + u] >> 16));
+            for (int u = 0; u < SETS; ++u) {
+              uint32_t kb[4];
+              ldsm4(kb, chunk(stage + part_off[u], r0[u] + kr, k + ((lane >> 3) & 1)));
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                const uint32_t a[4] = {qa[k + v][0], NT == 2 ? qa[k + v][1] : 0u, qa[k + v][NT],
+                                       NT == 2 ? qa[k + v][2 * NT - 1] : 0u};
+                mma16816<true>(sc[u][0], a, e4m3x2_to_f16x2(kb[v]), e4m3x2_to_f16x2(kb[v] >> 16));
+                mma16816<true>(sc[u][1], a, e4m3x2_to_f16x2(kb[2 + v]), e4m3x2_to_f16x2(kb[2 + v] >> 16));
+              }
             }
           }
         }
-        // softmax over this warp's 16 keys, base 2
-        uint32_t pa[NT][4];
+        // softmax over this warp's keys, base 2
+        uint32_t pa[SETS][NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float x[4] = {sc[0][2 * t] * mult[t], sc[0][2 * t + 1] * mult[t], sc[1][2 * t] * mult[t],
-                        sc[1][2 * t + 1] * mult[t]};
-          if (live < 16) {
+          float x[SETS][4], mx = kNegInf;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((e >> 1) * 8 + i4 * 2 + (e & 1) >= live) x[e] = kNegInf;
+          for (int u = 0; u < SETS; ++u) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[u][e] = sc[u][e >> 1][2 * t + (e & 1)] * mult[t];
+              if (least < 16 && (e >> 1) * 8 + i4 * 2 + (e & 1) >= live[u]) x[u][e] = kNegInf;
+              mx = fmaxf(mx, x[u][e]);
+            }
+            if (p.logits != nullptr && hr + 8 * t < heads) {
+              float* row = p.logits + ((long long)at.b * p.Hq + h0 + hr + 8 * t) * p.cache.capacity() +
+                           t_first + k0[u] + i4 * 2;
+              // a slot pair starts at an even slot, and the capacity is even
+              if (i4 * 2 < live[u]) *reinterpret_cast<float2*>(row) = make_float2(x[u][0], x[u][1]);
+              if (8 + i4 * 2 < live[u]) *reinterpret_cast<float2*>(row + 8) = make_float2(x[u][2], x[u][3]);
+            }
           }
-          if (p.logits != nullptr && hr + 8 * t < heads) {
-            float* row = p.logits + ((long long)at.b * p.Hq + h0 + hr + 8 * t) * p.cache.capacity() +
-                         j0 + i4 * 2;
-            // a slot pair starts at an even slot, and the capacity is even
-            if (i4 * 2 < live) *reinterpret_cast<float2*>(row) = make_float2(x[0], x[1]);
-            if (8 + i4 * 2 < live) *reinterpret_cast<float2*>(row + 8) = make_float2(x[2], x[3]);
-          }
-          float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float m_new = fmaxf(m[t], mx);
-          if (__any_sync(0xffffffffu, m_new != m[t])) {
-            const float f = m_new == kNegInf ? 1.f : ex2(m[t] - m_new);
+          // the reference follows a row's maximum only when that has outgrown it by 2^8:
+          // the weights stay below 2^8 and a rescaling of O becomes rare
+          const bool grow = mx > m[t] + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2(m[t] - mx) : 1.f;
             l[t] *= f;
 #pragma unroll
             for (int c = 0; c < C / 8; ++c) {
               o[t][c][0] *= f; o[t][c][1] *= f; o[t][c][2] *= f; o[t][c][3] *= f;
             }
-            m[t] = m_new;
+            if (grow) m[t] = mx;
           }
-          const float ref = m_new == kNegInf ? 0.f : m_new;
-          // one rounding between the logit and the exponential: the product again, fused
+          const float ref = m[t] == kNegInf ? 0.f : m[t];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = x[e] == kNegInf ? 0.f : ex2(fmaf(sc[e >> 1][2 * t + (e & 1)], mult[t], -ref));
-          l[t] += (x[0] + x[1]) + (x[2] + x[3]);
-          split_pair<FP8>(x[0], x[1], &pa[t][0], &pa[t][1]);
-          split_pair<FP8>(x[2], x[3], &pa[t][2], &pa[t][3]);
+          for (int u = 0; u < SETS; ++u) {
+            // one rounding between the logit and the exponential: the product again, fused
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[u][e] = x[u][e] == kNegInf
+                            ? 0.f : ex2(fmaf(sc[u][e >> 1][2 * t + (e & 1)], mult[t], -ref));
+            l[t] += (x[u][0] + x[u][1]) + (x[u][2] + x[u][3]);
+            split_pair<FP8>(x[u][0], x[u][1], &pa[u][t][0], &pa[u][t][1]);
+            split_pair<FP8>(x[u][2], x[u][3], &pa[u][t][2], &pa[u][t][3]);
+          }
         }
         // O += P V
-        const int vr = r0 + (((lane >> 3) & 1) << 3) + (lane & 7);
-        if (!FP8) {
+        const int vr = (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            uint32_t vb[4];
-            ldsm4t(vb, chunk(sV, vr, 2 * k + (lane >> 4)));
+        for (int u = 0; u < SETS; ++u) {
+          const uint32_t sV = stage + L::kTile + part_off[u];
+          if (!FP8) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              mma16816<false>(o[t][2 * k], pa[t], vb[0], vb[1]);
-              mma16816<false>(o[t][2 * k + 1], pa[t], vb[2], vb[3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < kSteps; k += 2) {
-            uint32_t vb[4];
-            ldsm4t(vb, chunk(sV, vr, k + (lane >> 4)));
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              // a register holds columns (2n, 2n+1) of two keys: regroup by column
-              const uint32_t lo = __byte_perm(vb[2 * u], 0, 0x3120);
-              const uint32_t hi = __byte_perm(vb[2 * u + 1], 0, 0x3120);
-              const uint32_t e0 = e4m3x2_to_f16x2(lo), e1 = e4m3x2_to_f16x2(hi);
-              const uint32_t d0 = e4m3x2_to_f16x2(lo >> 16), d1 = e4m3x2_to_f16x2(hi >> 16);
+            for (int k = 0; k < kSteps; ++k) {
+              uint32_t vb[4];
+              ldsm4t(vb, chunk(sV, r0[u] + vr, 2 * k + (lane >> 4)));
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                mma16816<true>(o[t][2 * (k + u)], pa[t], e0, e1);
-                mma16816<true>(o[t][2 * (k + u) + 1], pa[t], d0, d1);
+                mma16816<false>(o[t][2 * k], pa[u][t], vb[0], vb[1]);
+                mma16816<false>(o[t][2 * k + 1], pa[u][t], vb[2], vb[3]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kSteps; k += 2) {
+              uint32_t vb[4];
+              ldsm4t(vb, chunk(sV, r0[u] + vr, k + (lane >> 4)));
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                // a register holds columns (2n, 2n+1) of two keys: regroup by column
+                const uint32_t lo = __byte_perm(vb[2 * v], 0, 0x3120);
+                const uint32_t hi = __byte_perm(vb[2 * v + 1], 0, 0x3120);
+                const uint32_t e0 = e4m3x2_to_f16x2(lo), e1 = e4m3x2_to_f16x2(hi);
+                const uint32_t d0 = e4m3x2_to_f16x2(lo >> 16), d1 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  mma16816<true>(o[t][2 * (k + v)], pa[u][t], e0, e1);
+                  mma16816<true>(o[t][2 * (k + v) + 1], pa[u][t], d0, d1);
+                }
               }
             }
           }
         }
         // the zeroed rows were written through the generic proxy: order them before
         // the next TMA write to this stage
-        if (live < 16) fence_proxy_async_smem();
+        if (least < 16) fence_proxy_async_smem();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
@@ -567,14 +619,34 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
       if (at.tile == 0) p.seg[item].x = blockIdx.x;
       if (at.tile + seg_tiles == at.tiles) p.seg[item].y = blockIdx.x;
     }
-    if (n < mine) dec_next_item(p.cache, at, per);
+    if (n < mine) dec_next_item<L::kKeys>(p.cache, at, per);
   }
 }
 
 // ------------------------------------------------------------------- join
+// (maximum, sum) of one row over n partials, in log2 units, by one warp: the lanes read
+// the partials side by side, so a row of many costs a few load latencies, not n.
+__device__ __forceinline__ float2 dec_row_stat(const float2* ml, int rows, int n, int lane) {
+  float top = kNegInf, sum = 0.f;
+#pragma unroll 4
+  for (int s = lane; s < n; s += 32) top = fmaxf(top, ml[(long long)s * rows].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == kNegInf ? 0.f : top;
+#pragma unroll 4
+  for (int s = lane; s < n; s += 32) {
+    const float2 v = ml[(long long)s * rows];
+    sum += ex2(v.x - ref) * v.y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return make_float2(ref, sum);
+}
+
 // Blocks [0, B * Hq): output and lse of one query head from its partials. The others
 // (weights): acc_out[slot] = acc[slot] + sum over the group's heads of the slot's
 // softmax weight, from the logits of the split kernel and the joined statistics.
+// Launched as a programmatic dependent of the split kernel.
 template <int C>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_per_tile,
@@ -584,49 +656,40 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hq = p.Hq, per = p.cache.Hkv * p.HT;
   const int n_join = p.cache.B * Hq;
+  grid_dependency_wait();
 
   if ((int)blockIdx.x < n_join) {
     const int b = blockIdx.x / Hq, h = blockIdx.x - b * Hq;
     const int kvh = h / p.G, g = h - kvh * p.G;
-    bf16* out = p.O + (long long)blockIdx.x * C;
-    if (p.cache.length(b) == 0) {      // no key: o = 0, lse = -inf
-      if (tid < C) out[tid] = __float2bfloat16(0.f);
-      if (tid == 0) {
-        if (p.lse != nullptr) p.lse[blockIdx.x] = kNegInf;
-        if (!p.cache.length_valid(b)) raise_device_error(kErrInvalid);
-      }
-      return;
-    }
-    if (tid == 0 && !p.cache.length_valid(b)) raise_device_error(kErrInvalid);
     const int item = b * per + kvh * p.HT + g / heads_per_tile;
     const int row = g % heads_per_tile;
+    bf16* out = p.O + (long long)blockIdx.x * C;
+    if (tid == 0 && !p.cache.length_valid(b)) raise_device_error(kErrInvalid);
+    if (p.cache.length(b) == 0) {      // no key: o = 0, lse = -inf
+      if (tid < C) out[tid] = __float2bfloat16(0.f);
+      if (tid == 0 && p.lse != nullptr) p.lse[blockIdx.x] = kNegInf;
+      return;
+    }
     const int2 seg = p.seg[item];
     if (seg.x == seg.y) return;        // one CTA had the whole item and finished it
-    const long long s0 = (long long)seg.x + item;
     const int n = seg.y - seg.x + 1;
-    float top = kNegInf;
-    for (int s = 0; s < n; ++s) top = fmaxf(top, p.part_ml[(s0 + s) * rows + row].x);
-    const float ref = top == kNegInf ? 0.f : top;
+    const float2* ml = p.part_ml + ((long long)seg.x + item) * rows + row;
+    const float* po = p.part_o + (((long long)seg.x + item) * rows + row) * C;
+    const float2 st = dec_row_stat(ml, rows, n, lane);       // every warp for itself
     constexpr int kGroups = kJoinThreads / C;
     const int c = tid % C, gr = tid / C;
-    float sum = 0.f, y = 0.f;
-    for (int s = 0; s < n; ++s) {
-      const float2 ml = p.part_ml[(s0 + s) * rows + row];
-      sum += ex2(ml.x - ref) * ml.y;
-    }
-#pragma unroll 4
-    for (int s = gr; s < n; s += kGroups) {
-      const float f = ex2(p.part_ml[(s0 + s) * rows + row].x - ref);
-      y += f * p.part_o[((s0 + s) * rows + row) * C + c];
-    }
+    float y = 0.f;
+#pragma unroll 8
+    for (int s = gr; s < n; s += kGroups)
+      y += ex2(ml[(long long)s * rows].x - st.x) * po[(long long)s * rows * C + c];
     red[tid] = y;
     __syncthreads();
     if (gr == 0) {
 #pragma unroll
       for (int k = 1; k < kGroups; ++k) y += red[k * C + c];
-      out[c] = __float2bfloat16(sum == 0.f ? 0.f : y / sum);
+      out[c] = __float2bfloat16(st.y == 0.f ? 0.f : y / st.y);
       if (c == 0 && p.lse != nullptr)
-        p.lse[blockIdx.x] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
+        p.lse[blockIdx.x] = st.y == 0.f ? kNegInf : (st.x + log2f(st.y)) * kLn2;
     }
     return;
   }
@@ -636,37 +699,42 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
   const int pair = wb / weight_blocks, first = wb - pair * weight_blocks;
   const int b = pair / p.cache.Hkv, kvh = pair - b * p.cache.Hkv;
   const int len = p.cache.length(b);
-  if (first * kJoinThreads >= len) return;
+  if (first * (kJoinThreads * 4) >= len) return;
   // base-2 log-sum-exp of every head of the group
   for (int g = warp; g < p.G; g += kJoinThreads / 32) {
     const int item = b * per + kvh * p.HT + g / heads_per_tile;
-    const int row = g % heads_per_tile;
     const int2 seg = p.seg[item];
-    const long long s0 = (long long)seg.x + item;
-    const int n = seg.y - seg.x + 1;
-    float top = kNegInf, sum = 0.f;
-    for (int s = lane; s < n; s += 32) top = fmaxf(top, p.part_ml[(s0 + s) * rows + row].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == kNegInf ? 0.f : top;
-    for (int s = lane; s < n; s += 32) {
-      const float2 ml = p.part_ml[(s0 + s) * rows + row];
-      sum += ex2(ml.x - ref) * ml.y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float2 st = dec_row_stat(p.part_ml + ((long long)seg.x + item) * rows + g % heads_per_tile,
+                                   rows, seg.y - seg.x + 1, lane);
     // +inf: every weight of this head is 0 (it saw no mass)
-    if (lane == 0) stat[g] = sum == 0.f ? -kNegInf : ref + log2f(sum);
+    if (lane == 0) stat[g] = st.y == 0.f ? -kNegInf : st.x + log2f(st.y);
   }
   __syncthreads();
-  const float* logits = p.logits + ((long long)b * Hq + kvh * p.G) * p.cache.capacity();
-  for (int j = first * kJoinThreads + tid; j < len; j += weight_blocks * kJoinThreads) {
+  const int cap = p.cache.capacity();
+  const float* logits = p.logits + ((long long)b * Hq + kvh * p.G) * cap;
+  // four neighbouring slots per thread (never across a page): 16-byte loads
+  for (int j = (first * kJoinThreads + tid) * 4; j < len; j += weight_blocks * kJoinThreads * 4) {
     const long long at = p.cache.slot_index(b, kvh, j);
     if (at < 0) continue;              // the split kernel raised the error
-    float w = 0.f;
+    const float4 old = *reinterpret_cast<const float4*>(p.cache.acc + at);
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int g = 0; g < p.G; ++g) w += ex2(logits[(long long)g * p.cache.capacity() + j] - stat[g]);
-    p.acc_out[at] = p.cache.acc[at] + w;
+    for (int g = 0; g < p.G; ++g) {
+      const float4 x = *reinterpret_cast<const float4*>(logits + (long long)g * cap + j);
+      const float l = stat[g];
+      w.x += ex2(x.x - l);
+      w.y += ex2(x.y - l);
+      w.z += ex2(x.z - l);
+      w.w += ex2(x.w - l);
+    }
+    w = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+    if (j + 4 <= len) {
+      *reinterpret_cast<float4*>(p.acc_out + at) = w;
+    } else {                           // the slots behind the end stay as they were
+      p.acc_out[at] = w.x;
+      if (j + 1 < len) p.acc_out[at + 1] = w.y;
+      if (j + 2 < len) p.acc_out[at + 2] = w.z;
+    }
   }
 }
 

@@ -800,3 +800,5 @@ def test_binding_refuses_on_the_gpu_too():
         xa.xattn_cache_evict(c, 10, ws)
     with pytest.raises(ValueError, match="CUDA"):
         xa.xattn_decode_attn(q, c, 0.1, o, ws.cpu())
+    with pytest.raises(AttributeError):
+        c.lens = c.lens.clone()
