@@ -204,7 +204,7 @@ DecodePlan decode_plan(const xattn_cache* c, int Hq, bool weights) {
   d.HT = (G + 15) / 16;
   d.rows = 8 * d.NT;
   d.items = (long long)c->B * c->Hkv * d.HT;
-  d.partials = d.items + kDecCtas;
+  d.partials = d.items + kDecMaxCtas;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   d.off_seg = up((size_t)d.partials * d.rows * sizeof(float2));
   d.off_o = d.off_seg + up((size_t)d.items * sizeof(int2));
@@ -249,7 +249,7 @@ int launch_decode_split(const CUtensorMap& mk, const CUtensorMap& mv, const Deco
   auto kern = decode_split_kernel<C, FP8, NT>;
   static unsigned long long done = 0;
   if (ensure_smem_limit(kern, L::kSmem, &done) != XATTN_OK) return XATTN_ECUDA;
-  kern<<<kDecCtas, kDecThreads, L::kSmem, st>>>(mk, mv, p);
+  kern<<<148 * L::kPerSm, kDecThreads, L::kSmem, st>>>(mk, mv, p);
   return launch_status();
 }
 

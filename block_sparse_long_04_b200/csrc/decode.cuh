@@ -14,19 +14,22 @@
 // decode_join_kernel. CTA c and item i meet in at most one segment, and along the linear
 // order c + i grows, so c + i numbers the partials.
 //
-// One CTA (two per SM): warp 4 loads K and V tiles by TMA, one box per page part, into
-// a ring of stages; warps 0-3 own a quarter of the tile's keys each and run
-// independently (own maximum, sum and output) until the item's end. The products use
-// warp-level MMAs: with Hq/Hkv <= 16 query rows the tensor work is a few percent of what
-// even that path offers, while a tcgen05 tile (M = 128) would hold 8 to 32 useful rows
-// and pass P and O through shared memory and TMEM between the steps.
-// The 16 rows of an MMA hold 8 heads twice in the P V product: rows 0-7 take the rounded
-// weights, rows 8-15 what the rounding left (p - round(p)), so the weights enter
-// with 16 (bf16) or 22 (f16) bits at no extra instruction, and o is rounded once.
+// One CTA (two or three per SM): warp 4 loads K and V tiles by TMA, one box per page part,
+// into a ring of stages; warps 0-3 own a quarter of the tile's keys each and run
+// independently (own reference, sum and output) until the item's end. The products use
+// warp-level MMAs with the cache as the A operand: S^T = K Q^T and O^T = V^T P^T, 16 keys
+// or columns by 8 heads, so the usual groups of 4 or 8 query heads fill the tile's N
+// (a tcgen05 tile would need M = 128 rows of queries, or P^T written to shared memory and
+// O^T read from TMEM between the steps; the tensor pipe is not what binds here). P turns
+// from the accumulator's layout into the B operand's with movmatrix, in registers.
 //
-// e4m3 pages are widened to f16, which holds them exactly. q is scaled by a power of two
-// per head so that its largest element is in [1/2, 1]; below 2^-14 of that f16 loses
-// bits, an error of 2^-25 of the largest element, less than the fp32 sums'.
+// Rounding. The weights enter P V as two 16-bit terms, p and what its rounding left (16 bits
+// together in bf16, 22 in f16), for one more MMA per tile; a single bf16 weight would add
+// an error as large as the output's own rounding. e4m3 pages are widened to f16, which
+// holds them exactly. q is scaled there by a power of two per head so that its largest
+// element is in [1/2, 1]; below 2^-14 of that f16 loses bits, an error of 2^-25 of the
+// largest element, less than the fp32 sums'. Sums, logits and statistics are fp32, o is
+// rounded once.
 //
 // Keys behind the end of a sequence inside its last page are masked, and their V rows
 // are zeroed in shared memory before use: 0 * NaN of a stale row would not be 0.
@@ -40,7 +43,7 @@
 namespace xattn {
 
 constexpr int kDecThreads = 160;      // four MMA warps, one TMA warp
-constexpr int kDecCtas = 296;         // 148 SMs x 2
+constexpr int kDecMaxCtas = 444;      // 148 SMs x 3
 constexpr int kJoinThreads = 512;
 constexpr int kDecMaxGroup = 128;     // query heads per kv head
 
@@ -59,27 +62,27 @@ struct DecodeParams {
   float scale_log2;
 };
 
-// Keys per tile: 64, or 128 where that fits a 32 KB stage and the registers: a warp
-// then works on two independent sets of 16 keys, which hides the latencies of its chain
-// (load, widen, product, maximum, exponential, product) and halves its overhead per key.
-// Ragged e4m3 batch of 32 (0.54 GB): 64 keys 128 us, 128 keys see below.
+// Keys per tile: 64, or 128 where a 32 KB stage holds them: a warp then works on two
+// independent sets of 16 keys, which hides the latencies of its chain (load, widen,
+// product, maximum, exponential, product) and halves its overhead per key.
 __host__ __device__ constexpr int dec_tile_keys(int C, bool fp8, int NT) {
   return NT == 1 && C * (fp8 ? 1 : 2) <= 128 ? 128 : 64;
 }
 
 template <int C, bool FP8, int NT>
 struct Decode {
+  static constexpr int kPerSm = NT == 1 ? 3 : 2;       // CTAs per SM (128 or 168 registers)
   static constexpr int kRow = C * (FP8 ? 1 : 2);
   static constexpr int kKeys = dec_tile_keys(C, FP8, NT);
   static constexpr int kSets = kKeys / 64;             // sets of 16 keys per warp
   static constexpr int kTile = kKeys * kRow;
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kFit = 98304 / kStage;
+  static constexpr int kFit = (NT == 1 ? 65536 : 98304) / kStage;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kRows = 8 * NT;                 // heads of one item
-  static constexpr int kFrag = C / 4;                  // output values per lane and head tile
-  static constexpr int kOffX = kStages * kStage;       // three warps' outputs
-  static constexpr int kOffMl = kOffX + 3 * kFrag * 32 * 4;
+  static constexpr int kXRow = C + 4;                  // fp32 output row, off the bank period
+  static constexpr int kOffX = kStages * kStage;       // [2][8][kXRow]
+  static constexpr int kOffMl = kOffX + 2 * 8 * kXRow * 4;
   static constexpr int kOffBar = kOffMl + 4 * kRows * 8;
   static constexpr int kSmem = kOffBar + 256 + 1024;   // + alignment slack
 };
@@ -191,6 +194,12 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint3
     *lo = pack_bf16x2(x - __uint_as_float(*hi << 16), y - __uint_as_float(*hi & 0xffff0000u));
   }
 }
+// transposes an 8 x 8 matrix of 16-bit values (lane l: row l/4, columns 2(l%4), +1)
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ void bar_mma_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -204,7 +213,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 
 // ------------------------------------------------------------------ split
 template <int C, bool FP8, int NT>
-__global__ void __launch_bounds__(kDecThreads, 2)
+__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
 decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ DecodeParams p) {
@@ -214,7 +223,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
   constexpr int kSteps = C / 16;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  float* xo = reinterpret_cast<float*>(smem + L::kOffX);        // [3][kFrag][32]
+  float* xo = reinterpret_cast<float*>(smem + L::kOffX);        // [2][8][kXRow]
   float2* xml = reinterpret_cast<float2*>(smem + L::kOffMl);    // [4][kRows]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t* empty = full + ST;
@@ -333,33 +342,33 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
     const bool whole = seg_tiles == at.tiles;
     const int item = at.b * per + at.hk;
 
-    // queries as the A operand: rows 0-7 heads 0-7, rows 8-15 heads 8-15 (NT = 2)
-    uint32_t qa[kSteps][2 * NT];
-    float mult[NT];
+    // queries as the B operand: lane holds head lane/4 (of the 8 of head tile t)
+    uint32_t qb[NT][kSteps][2];
+    float mult[NT][2];       // from product to log2 units, for this lane's heads 2i, 2i+1
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int h = hr + 8 * t;
       const bf16* q = p.q + (long long)at.b * p.q_sb + (long long)(h0 + h) * p.q_sh;
-      mult[t] = p.scale_log2;
       if (!FP8) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          qa[s][t] = h < heads ? *reinterpret_cast<const uint32_t*>(q + s * 16 + i4 * 2) : 0u;
-          qa[s][NT + t] = h < heads ? *reinterpret_cast<const uint32_t*>(q + s * 16 + i4 * 2 + 8) : 0u;
+          qb[t][s][0] = h < heads ? *reinterpret_cast<const uint32_t*>(q + s * 16 + i4 * 2) : 0u;
+          qb[t][s][1] = h < heads ? *reinterpret_cast<const uint32_t*>(q + s * 16 + i4 * 2 + 8) : 0u;
         }
+        mult[t][0] = mult[t][1] = p.scale_log2;
       } else {
         // four neighbouring elements per lane and step: the order in which e4m3 pairs
         // come out of a widened key row
-        uint2 raw[kSteps];
         float top = 0.f;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          raw[s] = h < heads ? *reinterpret_cast<const uint2*>(q + s * 16 + i4 * 4) : make_uint2(0u, 0u);
-          const uint32_t w[2] = {raw[s].x, raw[s].y};
+          const uint2 w = h < heads ? *reinterpret_cast<const uint2*>(q + s * 16 + i4 * 4) : make_uint2(0u, 0u);
+          qb[t][s][0] = w.x;
+          qb[t][s][1] = w.y;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            top = fmax3(top, fabsf(__uint_as_float(w[e] << 16)),
-                        fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+            top = fmax3(top, fabsf(__uint_as_float(qb[t][s][e] << 16)),
+                        fabsf(__uint_as_float(qb[t][s][e] & 0xffff0000u)));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -367,23 +376,25 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
         const int e = min(max((int)(__float_as_uint(top) >> 23) - 126, -126), 126);
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          qa[s][t] = pack_f16x2(__uint_as_float(raw[s].x << 16) * down,
-                                __uint_as_float(raw[s].x & 0xffff0000u) * down);
-          qa[s][NT + t] = pack_f16x2(__uint_as_float(raw[s].y << 16) * down,
-                                     __uint_as_float(raw[s].y & 0xffff0000u) * down);
-        }
-        mult[t] = p.scale_log2 * __ldg(p.cache.k_scale + kvh) * __uint_as_float((uint32_t)(127 + e) << 23);
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            qb[t][s][w] = pack_f16x2(__uint_as_float(qb[t][s][w] << 16) * down,
+                                     __uint_as_float(qb[t][s][w] & 0xffff0000u) * down);
+        const float back = p.scale_log2 * __ldg(p.cache.k_scale + kvh) * __uint_as_float((uint32_t)(127 + e) << 23);
+        mult[t][0] = __shfl_sync(0xffffffffu, back, i4 * 8);
+        mult[t][1] = __shfl_sync(0xffffffffu, back, i4 * 8 + 4);
       }
     }
 
-    float m[NT], l[NT], o[NT][C / 8][4];
+    // reference, sum of this lane's keys, and O^T (columns lane/4, +8 of each 16), per head
+    float m[NT][2], l[NT][2], o[NT][kSteps][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t] = kNegInf;
-      l[t] = 0.f;
+      m[t][0] = m[t][1] = kNegInf;
+      l[t][0] = l[t][1] = 0.f;
 #pragma unroll
-      for (int c = 0; c < C / 8; ++c) o[t][c][0] = o[t][c][1] = o[t][c][2] = o[t][c][3] = 0.f;
+      for (int c = 0; c < kSteps; ++c) o[t][c][0] = o[t][c][1] = o[t][c][2] = o[t][c][3] = 0.f;
     }
 
     for (int s = 0; s < seg_tiles; ++s, ++n) {
@@ -411,123 +422,129 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
             }
           __syncwarp();
         }
-        // S: rows heads, columns keys 0-7 and 8-15 of each set
-        float sc[SETS][2][4];
+        // S^T: rows keys, columns heads
+        float sc[SETS][NT][4];
 #pragma unroll
         for (int u = 0; u < SETS; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[u][0][e] = sc[u][1][e] = 0.f;
-        const int kr = ((lane >> 4) << 3) + (lane & 7);
-        if (!FP8) {
+          for (int t = 0; t < NT; ++t) sc[u][t][0] = sc[u][t][1] = sc[u][t][2] = sc[u][t][3] = 0.f;
+        const int row_a = (((lane >> 3) & 1) << 3) + (lane & 7);   // matrices: rows, then chunks
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            const uint32_t a[4] = {qa[k][0], NT == 2 ? qa[k][1] : 0u, qa[k][NT],
-                                   NT == 2 ? qa[k][2 * NT - 1] : 0u};
+        for (int k = 0; k < kSteps; k += FP8 ? 2 : 1) {
 #pragma unroll
-            for (int u = 0; u < SETS; ++u) {
-              uint32_t kb[4];
-              ldsm4(kb, chunk(stage + part_off[u], r0[u] + kr, 2 * k + ((lane >> 3) & 1)));
-              mma16816<false>(sc[u][0], a, kb[0], kb[1]);
-              mma16816<false>(sc[u][1], a, kb[2], kb[3]);
-            }
-          }
-        } else {
+          for (int u = 0; u < SETS; ++u) {
+            uint32_t r[4];
+            ldsm4(r, chunk(stage + part_off[u], r0[u] + row_a, (FP8 ? k : 2 * k) + (lane >> 4)));
+            if (!FP8) {
 #pragma unroll
-          for (int k = 0; k < kSteps; k += 2) {
-#pragma unroll
-            for (int u = 0; u < SETS; ++u) {
-              uint32_t kb[4];
-              ldsm4(kb, chunk(stage + part_off[u], r0[u] + kr, k + ((lane >> 3) & 1)));
+              for (int t = 0; t < NT; ++t) mma16816<false>(sc[u][t], r, qb[t][k][0], qb[t][k][1]);
+            } else {
 #pragma unroll
               for (int v = 0; v < 2; ++v) {
-                const uint32_t a[4] = {qa[k + v][0], NT == 2 ? qa[k + v][1] : 0u, qa[k + v][NT],
-                                       NT == 2 ? qa[k + v][2 * NT - 1] : 0u};
-                mma16816<true>(sc[u][0], a, e4m3x2_to_f16x2(kb[v]), e4m3x2_to_f16x2(kb[v] >> 16));
-                mma16816<true>(sc[u][1], a, e4m3x2_to_f16x2(kb[2 + v]), e4m3x2_to_f16x2(kb[2 + v] >> 16));
+                const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * v]), e4m3x2_to_f16x2(r[2 * v + 1]),
+                                       e4m3x2_to_f16x2(r[2 * v] >> 16),
+                                       e4m3x2_to_f16x2(r[2 * v + 1] >> 16)};
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                  mma16816<true>(sc[u][t], a, qb[t][k + v][0], qb[t][k + v][1]);
               }
             }
           }
         }
-        // softmax over this warp's keys, base 2
-        uint32_t pa[SETS][NT][4];
+        // softmax over this warp's keys, base 2; value e: key lane/4 + 8 (e/2), head 2i + e%2
+        uint32_t pb[SETS][NT][4];        // P^T as the B operand: rounded, remainder
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float x[SETS][4], mx = kNegInf;
+          float x[SETS][4], mx[2] = {kNegInf, kNegInf};
 #pragma unroll
           for (int u = 0; u < SETS; ++u) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              x[u][e] = sc[u][e >> 1][2 * t + (e & 1)] * mult[t];
-              if (least < 16 && (e >> 1) * 8 + i4 * 2 + (e & 1) >= live[u]) x[u][e] = kNegInf;
-              mx = fmaxf(mx, x[u][e]);
+              x[u][e] = sc[u][t][e] * mult[t][e & 1];
+              if (least < 16 && hr + 8 * (e >> 1) >= live[u]) x[u][e] = kNegInf;
+              mx[e & 1] = fmaxf(mx[e & 1], x[u][e]);
             }
-            if (p.logits != nullptr && hr + 8 * t < heads) {
-              float* row = p.logits + ((long long)at.b * p.Hq + h0 + hr + 8 * t) * p.cache.capacity() +
-                           t_first + k0[u] + i4 * 2;
-              // a slot pair starts at an even slot, and the capacity is even
-              if (i4 * 2 < live[u]) *reinterpret_cast<float2*>(row) = make_float2(x[u][0], x[u][1]);
-              if (8 + i4 * 2 < live[u]) *reinterpret_cast<float2*>(row + 8) = make_float2(x[u][2], x[u][3]);
-            }
-          }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          // the reference follows a row's maximum only when that has outgrown it by 2^8:
-          // the weights stay below 2^8 and a rescaling of O becomes rare
-          const bool grow = mx > m[t] + 8.f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? ex2(m[t] - mx) : 1.f;
-            l[t] *= f;
+            if (p.logits != nullptr) {
 #pragma unroll
-            for (int c = 0; c < C / 8; ++c) {
-              o[t][c][0] *= f; o[t][c][1] *= f; o[t][c][2] *= f; o[t][c][3] *= f;
+              for (int e = 0; e < 4; ++e) {
+                const int h = i4 * 2 + (e & 1) + 8 * t, j = hr + 8 * (e >> 1);
+                if (h < heads && j < live[u])
+                  p.logits[((long long)at.b * p.Hq + h0 + h) * p.cache.capacity() + t_first + k0[u] + j] = x[u][e];
+              }
             }
-            if (grow) m[t] = mx;
           }
-          const float ref = m[t] == kNegInf ? 0.f : m[t];
+#pragma unroll
+          for (int d = 0; d < 2; ++d)
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mx[d] = fmaxf(mx[d], __shfl_xor_sync(0xffffffffu, mx[d], w));
+          // the reference follows a head's maximum only when that has outgrown it by 2^8:
+          // the weights stay below 2^8 and a rescaling of O becomes rare
+          const bool grow[2] = {mx[0] > m[t][0] + 8.f, mx[1] > m[t][1] + 8.f};
+          if (__any_sync(0xffffffffu, grow[0] || grow[1])) {
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              const float f = grow[d] ? ex2(m[t][d] - mx[d]) : 1.f;
+              l[t][d] *= f;
+#pragma unroll
+              for (int c = 0; c < kSteps; ++c) {
+                o[t][c][d] *= f;
+                o[t][c][2 + d] *= f;
+              }
+              if (grow[d]) m[t][d] = mx[d];
+            }
+          }
+          const float ref[2] = {m[t][0] == kNegInf ? 0.f : m[t][0], m[t][1] == kNegInf ? 0.f : m[t][1]};
 #pragma unroll
           for (int u = 0; u < SETS; ++u) {
             // one rounding between the logit and the exponential: the product again, fused
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              x[u][e] = x[u][e] == kNegInf
-                            ? 0.f : ex2(fmaf(sc[u][e >> 1][2 * t + (e & 1)], mult[t], -ref));
-            l[t] += (x[u][0] + x[u][1]) + (x[u][2] + x[u][3]);
-            split_pair<FP8>(x[u][0], x[u][1], &pa[u][t][0], &pa[u][t][1]);
-            split_pair<FP8>(x[u][2], x[u][3], &pa[u][t][2], &pa[u][t][3]);
+              x[u][e] = x[u][e] == kNegInf ? 0.f : ex2(fmaf(sc[u][t][e], mult[t][e & 1], -ref[e & 1]));
+            l[t][0] += x[u][0] + x[u][2];
+            l[t][1] += x[u][1] + x[u][3];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float y0 = x[u][2 * w], y1 = x[u][2 * w + 1];
+              uint32_t hi, lo;
+              split_pair<FP8>(y0, y1, &hi, &lo);
+              pb[u][t][w] = transpose8x8(hi);
+              pb[u][t][2 + w] = transpose8x8(lo);
+            }
           }
         }
-        // O += P V
-        const int vr = (((lane >> 3) & 1) << 3) + (lane & 7);
+        // O^T += V^T P^T
 #pragma unroll
         for (int u = 0; u < SETS; ++u) {
           const uint32_t sV = stage + L::kTile + part_off[u];
           if (!FP8) {
+            const int row_v = ((lane >> 4) << 3) + (lane & 7);
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-              uint32_t vb[4];
-              ldsm4t(vb, chunk(sV, r0[u] + vr, 2 * k + (lane >> 4)));
+              uint32_t a[4];
+              ldsm4t(a, chunk(sV, r0[u] + row_v, 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                mma16816<false>(o[t][2 * k], pa[u][t], vb[0], vb[1]);
-                mma16816<false>(o[t][2 * k + 1], pa[u][t], vb[2], vb[3]);
+                mma16816<false>(o[t][k], a, pb[u][t][0], pb[u][t][1]);
+                mma16816<false>(o[t][k], a, pb[u][t][2], pb[u][t][3]);
               }
             }
           } else {
 #pragma unroll
             for (int k = 0; k < kSteps; k += 2) {
-              uint32_t vb[4];
-              ldsm4t(vb, chunk(sV, r0[u] + vr, k + (lane >> 4)));
+              uint32_t r[4];
+              ldsm4t(r, chunk(sV, r0[u] + row_a, k + (lane >> 4)));
 #pragma unroll
               for (int v = 0; v < 2; ++v) {
-                // a register holds columns (2n, 2n+1) of two keys: regroup by column
-                const uint32_t lo = __byte_perm(vb[2 * v], 0, 0x3120);
-                const uint32_t hi = __byte_perm(vb[2 * v + 1], 0, 0x3120);
-                const uint32_t e0 = e4m3x2_to_f16x2(lo), e1 = e4m3x2_to_f16x2(hi);
-                const uint32_t d0 = e4m3x2_to_f16x2(lo >> 16), d1 = e4m3x2_to_f16x2(hi >> 16);
+                // a register holds columns (2n, 2n+1) of two keys: regroup by column; the
+                // MMA's rows 0-7 take the even columns, rows 8-15 the odd ones
+                const uint32_t lo = __byte_perm(r[2 * v], 0, 0x3120);
+                const uint32_t hi = __byte_perm(r[2 * v + 1], 0, 0x3120);
+                const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16),
+                                       e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                  mma16816<true>(o[t][2 * (k + v)], pa[u][t], e0, e1);
-                  mma16816<true>(o[t][2 * (k + v) + 1], pa[u][t], d0, d1);
+                  mma16816<true>(o[t][k + v], a, pb[u][t][0], pb[u][t][1]);
+                  mma16816<true>(o[t][k + v], a, pb[u][t][2], pb[u][t][3]);
                 }
               }
             }
@@ -543,77 +560,93 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
 
     // ------------------------------------------- the four warps' outputs join
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
-      l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
-      if (i4 == 0) xml[warp * L::kRows + hr + 8 * t] = make_float2(m[t], l[t]);
-    }
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[t][d] += __shfl_xor_sync(0xffffffffu, l[t][d], w);
+        if (hr == 0) xml[warp * L::kRows + 8 * t + 2 * i4 + d] = make_float2(m[t][d], l[t][d]);
+      }
     bar_mma_warps();
     const long long slot = (long long)blockIdx.x + item;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float top = kNegInf, sum = 0.f;
-      const int row = hr + 8 * t;
+      // every warp's output against the largest reference, in two rounds through the two
+      // buffers: warps 2 and 3 write, warps 0 and 1 add theirs
+      float f[2];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) top = fmaxf(top, xml[w * L::kRows + row].x);
+      for (int d = 0; d < 2; ++d) {
+        float all = kNegInf;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) all = fmaxf(all, xml[w * L::kRows + 8 * t + 2 * i4 + d].x);
+        f[d] = ex2(m[t][d] - (all == kNegInf ? 0.f : all));
+      }
+      // in the end 16 lanes per head write C/16 columns each; the statistics are read
+      // before the rounds' barriers, behind which a faster warp may write the next item's
+      const int row = tid >> 4, g = row + 8 * t, c0 = (tid & 15) * (C / 16);
+      float top = kNegInf, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, xml[w * L::kRows + g].x);
       const float ref = top == kNegInf ? 0.f : top;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float2 ml = xml[w * L::kRows + row];
+        const float2 ml = xml[w * L::kRows + g];
         sum += ex2(ml.x - ref) * ml.y;
       }
-      const float f = ex2(m[t] - ref);
-      if (t > 0) bar_mma_warps();      // the previous head tile's values have been read
-      if (warp > 0) {
+      float* buf = xo + (warp & 1) * 8 * L::kXRow;
 #pragma unroll
-        for (int c = 0; c < C / 8; ++c) {
-          xo[((warp - 1) * L::kFrag + 2 * c) * 32 + lane] = (o[t][c][0] + o[t][c][2]) * f;
-          xo[((warp - 1) * L::kFrag + 2 * c + 1) * 32 + lane] = (o[t][c][1] + o[t][c][3]) * f;
+      for (int round = 0; round < 2; ++round) {
+        if ((warp >> 1) == 1 - round) {
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // e4m3: rows 0-7 of the tile are its even columns, rows 8-15 the odd ones
+              const int col = c * 16 + (FP8 ? 2 * hr + (e >> 1) : hr + 8 * (e >> 1));
+              float* y = buf + (2 * i4 + (e & 1)) * L::kXRow + col;
+              const float v = o[t][c][e] * f[e & 1];
+              *y = round == 0 ? v : *y + v;
+            }
         }
+        bar_mma_warps();
       }
-      bar_mma_warps();
-      if (warp == 0 && row < heads) {
+      if (g < heads) {
         const float vs = FP8 ? __ldg(p.cache.v_scale + kvh) : 1.f;
         const float inv = whole ? vs / sum : vs;
+        const float* x0 = xo + row * L::kXRow + c0;
+        const float* x1 = x0 + 8 * L::kXRow;
+        float y[C / 16];
 #pragma unroll
-        for (int c = 0; c < C / 8; c += 2) {
-          float y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int cc = c + (e >> 1), d = e & 1;
-            y[e] = (o[t][cc][d] + o[t][cc][d + 2]) * f;
-#pragma unroll
-            for (int w = 0; w < 3; ++w) y[e] += xo[(w * L::kFrag + 2 * cc + d) * 32 + lane];
-            y[e] = sum == 0.f ? 0.f : y[e] * inv;      // no mass: o = 0
-          }
-          // bf16: columns 8c + 2i, +1 and 8(c+1) + 2i, +1; e4m3: 8c + 4i .. +3, even and
-          // odd columns in neighbouring tiles
-          if (whole) {
-            bf16* out = p.O + ((long long)at.b * p.Hq + h0 + row) * C;
-            if (FP8) {
-              *reinterpret_cast<uint2*>(out + c * 8 + i4 * 4) =
-                  make_uint2(pack_bf16x2(y[0], y[2]), pack_bf16x2(y[1], y[3]));
-            } else {
-              *reinterpret_cast<uint32_t*>(out + c * 8 + i4 * 2) = pack_bf16x2(y[0], y[1]);
-              *reinterpret_cast<uint32_t*>(out + c * 8 + 8 + i4 * 2) = pack_bf16x2(y[2], y[3]);
-            }
-          } else {
-            float* out = p.part_o + (slot * L::kRows + row) * C;
-            if (FP8) {
-              *reinterpret_cast<float4*>(out + c * 8 + i4 * 4) = make_float4(y[0], y[2], y[1], y[3]);
-            } else {
-              *reinterpret_cast<float2*>(out + c * 8 + i4 * 2) = make_float2(y[0], y[1]);
-              *reinterpret_cast<float2*>(out + c * 8 + 8 + i4 * 2) = make_float2(y[2], y[3]);
-            }
-          }
+        for (int c = 0; c < C / 16; c += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(x0 + c);
+          const float4 b = *reinterpret_cast<const float4*>(x1 + c);
+          y[c] = (a.x + b.x) * inv;
+          y[c + 1] = (a.y + b.y) * inv;
+          y[c + 2] = (a.z + b.z) * inv;
+          y[c + 3] = (a.w + b.w) * inv;
         }
-        if (i4 == 0) {
-          p.part_ml[slot * L::kRows + row] = make_float2(top, sum);
+        if (sum == 0.f)          // no mass: o = 0
+#pragma unroll
+          for (int c = 0; c < C / 16; ++c) y[c] = 0.f;
+        if (whole) {
+          bf16* out = p.O + ((long long)at.b * p.Hq + h0 + g) * C + c0;
+#pragma unroll
+          for (int c = 0; c < C / 16; c += 4)
+            *reinterpret_cast<uint2*>(out + c) =
+                make_uint2(pack_bf16x2(y[c], y[c + 1]), pack_bf16x2(y[c + 2], y[c + 3]));
+        } else {
+          float* out = p.part_o + (slot * L::kRows + g) * C + c0;
+#pragma unroll
+          for (int c = 0; c < C / 16; c += 4)
+            *reinterpret_cast<float4*>(out + c) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
+        }
+        if ((tid & 15) == 0) {
+          p.part_ml[slot * L::kRows + g] = make_float2(top, sum);
           if (whole && p.lse != nullptr)
-            p.lse[(long long)at.b * p.Hq + h0 + row] =
-                sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
+            p.lse[(long long)at.b * p.Hq + h0 + g] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
       }
+      if (t + 1 < NT) bar_mma_warps();      // the buffers have been read
     }
     if (tid == 0) {
       if (at.tile == 0) p.seg[item].x = blockIdx.x;

@@ -12,8 +12,11 @@
 // CTA owns a tile of tokens of one sequence and ALL their heads: the sines of a token
 // are computed once, into shared memory, and serve its Hq + Hkv heads (for 32 + 8 heads
 // the 64-bit work is 1/40 per row). A row is C/16 threads, each with two 16-byte chunks
-// (the two halves of its pairs when the pairs are split across the row), and a thread
-// keeps two rows in flight.
+// (the two halves of its pairs when the pairs are split across the row). The rows of a
+// sweep are a multiple of the tile's tokens, so a thread meets the same token and the same
+// 8 pairs in every row: it takes their sines into registers once (from a table laid out so
+// that neighbouring threads read neighbouring words) and its loop over the heads holds
+// nothing but loads, 16 products and stores, with kUnroll rows in flight.
 //
 // Append. Token t of sequence b goes to slot lens[b] - n_new[b] + t; its page and row
 // are resolved once per token. A page id or slot out of range writes nothing and raises
@@ -80,13 +83,35 @@ struct RopeParams {
   int M, tokens_log2;
 };
 
-__device__ __forceinline__ uint2 pack_e4m3x8(const float* y, float scale) {
-  // division, not a product with a rounded reciprocal: one rounding before the e4m3 one
+// y / scale for the e4m3 conversion. The quotient must be the correctly rounded one: where it
+// falls on the middle between two e4m3 values, one unit too much or too little turns the
+// result. With r = RN(1/scale), q = RN(y r), the remainder y - q scale is exact in one FMA
+// and RN(q + remainder r) is the rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990),
+// as long as nothing over- or underflows: for scales between 2^-60 and 2^60 that leaves
+// quotients far outside e4m3's range, whose uncorrected q saturates (or vanishes) alike.
+// Other scales take the division itself.
+struct E4m3Scale {
+  float scale, inv;
+  bool plain;
+};
+__device__ __forceinline__ E4m3Scale e4m3_scale(float scale) {
+  const bool plain = !(scale > 0x1p-60f && scale < 0x1p60f);
+  return {scale, __frcp_rn(scale), plain};
+}
+__device__ __forceinline__ float e4m3_quotient(float y, const E4m3Scale& s) {
+  if (s.plain) return __fdiv_rn(y, s.scale);
+  const float q = y * s.inv;
+  const float exact = fmaf(fmaf(-q, s.scale, y), s.inv, q);
+  // q will do where it is zero (the correction would lose the sign of -0), beyond e4m3's
+  // largest, infinite or NaN: one comparison of the bits of |q|, 1024.f = 0x44800000
+  return (__float_as_uint(fabsf(q)) - 1u) < 0x447fffffu ? exact : q;
+}
+__device__ __forceinline__ uint2 pack_e4m3x8(const float* y, const E4m3Scale& s) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     w[i] = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(y[2 * i], scale), __fdiv_rn(y[2 * i + 1], scale)), __NV_SATFINITE,
+        make_float2(e4m3_quotient(y[2 * i], s), e4m3_quotient(y[2 * i + 1], s)), __NV_SATFINITE,
         __NV_E4M3);
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
@@ -110,7 +135,10 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kTpr = C / 16;                  // threads per row
   constexpr int kRows = kRopeThreads / kTpr;    // rows per sweep of the CTA
   constexpr int kUnroll = 2;
-  __shared__ float2 cs[ROPE ? kRopeMaxTokens * (C / 2) : 1];
+  // (cos, sin) of token t's pairs: 8 pairs of a thread lie C/16 apart; 8 words between tokens
+  // keep the tokens of a warp on different banks
+  constexpr int kCsRow = C / 2 + 8;
+  __shared__ float2 cs[ROPE ? kRopeMaxTokens * kCsRow : 1];
   __shared__ long long dst_row[kRopeMaxTokens];   // pool index at head 0, -1: none
 
   const int b = blockIdx.y, TT = 1 << p.tokens_log2;
@@ -163,7 +191,11 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
       const float half_turns = (float)(2.0 * (turns - rint(turns)));
       float s, c;
       sincospif(half_turns, &s, &c);
-      cs[i] = make_float2(c, s * p.sign);
+      // pair pr belongs to chunk pr/4 (interleaved; thread chunk % kTpr, its first or second
+      // one) or to thread pr/8
+      const int at = p.interleaved ? ((pr >> 2) / kTpr * 4 + (pr & 3)) * kTpr + (pr >> 2) % kTpr
+                                   : (pr & 7) * kTpr + (pr >> 3);
+      cs[t * kCsRow + at] = make_float2(c, s * p.sign);
     }
   }
   __syncthreads();
@@ -176,6 +208,15 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
     const int hp = rotated / 2;
     if (t8 < hp) { ca = t8; cb = t8 + hp; }
     else { ca = rotated + 2 * (t8 - hp); cb = ca + 1; }
+  }
+  const bool rope_a = ca < rotated, rope_b = cb < rotated;
+  float2 w[ROPE ? 8 : 1];
+  if (ROPE) {
+    // unused ones (chunks that pass through, tokens behind the tile's last) are never applied
+    const float2* row = cs + (lane_r & (TT - 1)) * kCsRow + t8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = (p.interleaved ? (i < 4 ? rope_a : rope_b) : rope_a) ? row[i * kTpr] : make_float2(1.f, 0.f);
   }
   const int nq = p.q.heads, nk = p.k.heads, nv = DST != 0 ? p.v.heads : 0;
   const int rows = (nq + nk + nv) << p.tokens_log2;
@@ -207,39 +248,27 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
       const bool is_q = h < nq, is_v = h >= nq + nk;
       float a[8], c[8];
       const bool raw_copy = DST != 2 || is_q;     // bf16 out: an unrotated chunk stays as it is
-      const bool rot_a = ROPE && !is_v && ca < rotated, rot_b = ROPE && !is_v && cb < rotated;
+      const bool rot_a = ROPE && !is_v && rope_a, rot_b = ROPE && !is_v && rope_b;
       if (rot_a || rot_b || !raw_copy) {
         unpack_bf16x8(xa[u], a);
         unpack_bf16x8(xb[u], c);
       }
       if (ROPE && !is_v) {
-        const float2* row = cs + tok[u] * p.pairs;
         if (p.interleaved) {
-          if (rot_a) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 w = row[ca * 4 + i];
-              const float x1 = a[2 * i], x2 = a[2 * i + 1];
-              a[2 * i] = x1 * w.x - x2 * w.y;
-              a[2 * i + 1] = x2 * w.x + x1 * w.y;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float a1 = a[2 * i], a2 = a[2 * i + 1], c1 = c[2 * i], c2 = c[2 * i + 1];
+            a[2 * i] = a1 * w[i].x - a2 * w[i].y;
+            a[2 * i + 1] = a2 * w[i].x + a1 * w[i].y;
+            c[2 * i] = c1 * w[4 + i].x - c2 * w[4 + i].y;
+            c[2 * i + 1] = c2 * w[4 + i].x + c1 * w[4 + i].y;
           }
-          if (rot_b) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 w = row[cb * 4 + i];
-              const float x1 = c[2 * i], x2 = c[2 * i + 1];
-              c[2 * i] = x1 * w.x - x2 * w.y;
-              c[2 * i + 1] = x2 * w.x + x1 * w.y;
-            }
-          }
-        } else if (rot_a) {          // cb = ca + pairs/8 holds the partners
+        } else {                     // cb = ca + pairs/8 holds the partners
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 w = row[ca * 8 + i];
             const float x1 = a[i], x2 = c[i];
-            a[i] = x1 * w.x - x2 * w.y;
-            c[i] = x2 * w.x + x1 * w.y;
+            a[i] = x1 * w[i].x - x2 * w[i].y;
+            c[i] = x2 * w[i].x + x1 * w[i].y;
           }
         }
       }
@@ -261,7 +290,7 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
           *reinterpret_cast<uint4*>(y + ca * 8) = rot_a ? pack_bf16x8(a) : xa[u];
           *reinterpret_cast<uint4*>(y + cb * 8) = rot_b ? pack_bf16x8(c) : xb[u];
         } else {
-          const float sc = __ldg((is_v ? p.cache.v_scale : p.cache.k_scale) + hh);
+          const E4m3Scale sc = e4m3_scale(__ldg((is_v ? p.cache.v_scale : p.cache.k_scale) + hh));
           uint8_t* y = static_cast<uint8_t*>(pages) + at;
           *reinterpret_cast<uint2*>(y + ca * 8) = pack_e4m3x8(a, sc);
           *reinterpret_cast<uint2*>(y + cb * 8) = pack_e4m3x8(c, sc);
