@@ -44,7 +44,7 @@ namespace xattn {
 
 constexpr int kDecThreads = 160;      // four MMA warps, one TMA warp
 constexpr int kDecMaxCtas = 444;      // 148 SMs x 3
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 128;    // four groups of partials x 32 columns
 constexpr int kDecMaxGroup = 128;     // query heads per kv head
 
 struct DecodeParams {
@@ -676,10 +676,12 @@ __device__ __forceinline__ float2 dec_row_stat(const float2* ml, int rows, int n
   return make_float2(ref, sum);
 }
 
-// Blocks [0, B * Hq): output and lse of one query head from its partials. The others
-// (weights): acc_out[slot] = acc[slot] + sum over the group's heads of the slot's
-// softmax weight, from the logits of the split kernel and the joined statistics.
-// Launched as a programmatic dependent of the split kernel.
+// Blocks [0, B * Hq * C/32): 32 columns of a query head's output, and its lse, from the
+// partials. The others (weights): acc_out[slot] = acc[slot] + sum over the group's heads of
+// the slot's softmax weight, from the logits of the split kernel and the joined statistics.
+// Launched as a programmatic dependent of the split kernel. Its time is a chain of
+// latencies (segment, statistics and values, sum), so the blocks are small, and the values
+// are loaded before the statistics that weigh them are known.
 template <int C>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_per_tile,
@@ -688,41 +690,49 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
   __shared__ float stat[kDecMaxGroup];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hq = p.Hq, per = p.cache.Hkv * p.HT;
-  const int n_join = p.cache.B * Hq;
+  const int n_join = p.cache.B * Hq * (C / 32);
   grid_dependency_wait();
 
   if ((int)blockIdx.x < n_join) {
-    const int b = blockIdx.x / Hq, h = blockIdx.x - b * Hq;
+    const int bh = blockIdx.x / (C / 32), c = (blockIdx.x % (C / 32)) * 32 + lane;
+    const int b = bh / Hq, h = bh - b * Hq;
     const int kvh = h / p.G, g = h - kvh * p.G;
     const int item = b * per + kvh * p.HT + g / heads_per_tile;
     const int row = g % heads_per_tile;
-    bf16* out = p.O + (long long)blockIdx.x * C;
-    if (tid == 0 && !p.cache.length_valid(b)) raise_device_error(kErrInvalid);
-    if (p.cache.length(b) == 0) {      // no key: o = 0, lse = -inf
-      if (tid < C) out[tid] = __float2bfloat16(0.f);
-      if (tid == 0 && p.lse != nullptr) p.lse[blockIdx.x] = kNegInf;
+    const bool first = c == 0 && warp == 0;
+    const int len = p.cache.length(b);
+    const int2 seg = p.seg[item];      // not written for a sequence without keys
+    if (first && !p.cache.length_valid(b)) raise_device_error(kErrInvalid);
+    if (len == 0) {                    // no key: o = 0, lse = -inf
+      if (warp == 0) p.O[(long long)bh * C + c] = __float2bfloat16(0.f);
+      if (first && p.lse != nullptr) p.lse[bh] = kNegInf;
       return;
     }
-    const int2 seg = p.seg[item];
     if (seg.x == seg.y) return;        // one CTA had the whole item and finished it
     const int n = seg.y - seg.x + 1;
     const float2* ml = p.part_ml + ((long long)seg.x + item) * rows + row;
-    const float* po = p.part_o + (((long long)seg.x + item) * rows + row) * C;
+    const float* po = p.part_o + (((long long)seg.x + item) * rows + row) * C + c;
+    constexpr int U = 8;
+    float v[U], m[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long s = warp + 4 * u;
+      v[u] = s < n ? po[s * rows * C] : 0.f;
+      m[u] = s < n ? ml[s * rows].x : kNegInf;
+    }
     const float2 st = dec_row_stat(ml, rows, n, lane);       // every warp for itself
-    constexpr int kGroups = kJoinThreads / C;
-    const int c = tid % C, gr = tid / C;
     float y = 0.f;
-#pragma unroll 8
-    for (int s = gr; s < n; s += kGroups)
-      y += ex2(ml[(long long)s * rows].x - st.x) * po[(long long)s * rows * C + c];
+#pragma unroll
+    for (int u = 0; u < U; ++u) y += ex2(m[u] - st.x) * v[u];
+#pragma unroll 4
+    for (long long s = warp + 4 * U; s < n; s += 4) y += ex2(ml[s * rows].x - st.x) * po[s * rows * C];
     red[tid] = y;
     __syncthreads();
-    if (gr == 0) {
-#pragma unroll
-      for (int k = 1; k < kGroups; ++k) y += red[k * C + c];
-      out[c] = __float2bfloat16(st.y == 0.f ? 0.f : y / st.y);
-      if (c == 0 && p.lse != nullptr)
-        p.lse[blockIdx.x] = st.y == 0.f ? kNegInf : (st.x + log2f(st.y)) * kLn2;
+    if (warp == 0) {
+      y = (red[lane] + red[32 + lane]) + (red[64 + lane] + red[96 + lane]);
+      p.O[(long long)bh * C + c] = __float2bfloat16(st.y == 0.f ? 0.f : y / st.y);
+      if (first && p.lse != nullptr)
+        p.lse[bh] = st.y == 0.f ? kNegInf : (st.x + log2f(st.y)) * kLn2;
     }
     return;
   }

@@ -15,8 +15,12 @@
 // (the two halves of its pairs when the pairs are split across the row). The rows of a
 // sweep are a multiple of the tile's tokens, so a thread meets the same token and the same
 // 8 pairs in every row: it takes their sines into registers once (from a table laid out so
-// that neighbouring threads read neighbouring words) and its loop over the heads holds
-// nothing but loads, 16 products and stores, with kUnroll rows in flight.
+// that neighbouring threads read neighbouring words), and its loop over the heads is a
+// strided copy with 16 products in it, four rows in flight. What the loop must not hold is
+// address arithmetic: with it, and the sines read per row, a 32K prompt of 32 + 8 heads
+// took 180 us, 120 us with the sines in registers, 110 us so (0.67 GB, 6.1 TB/s; the
+// 118784-token layer of 24 + 24 heads 443 us, 6.6 TB/s). Two resident CTAs with four
+// rows in flight and three with two measured alike, more CTAs slower.
 //
 // Append. Token t of sequence b goes to slot lens[b] - n_new[b] + t; its page and row
 // are resolved once per token. A page id or slot out of range writes nothing and raises
@@ -87,9 +91,9 @@ struct RopeParams {
 // falls on the middle between two e4m3 values, one unit too much or too little turns the
 // result. With r = RN(1/scale), q = RN(y r), the remainder y - q scale is exact in one FMA
 // and RN(q + remainder r) is the rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990),
-// as long as nothing over- or underflows: for scales between 2^-60 and 2^60 that leaves
-// quotients far outside e4m3's range, whose uncorrected q saturates (or vanishes) alike.
-// Other scales take the division itself.
+// as long as nothing over- or underflows: with scales between 2^-60 and 2^60 that leaves
+// quotients that vanish alike, and large ones. Those, and other scales, take the division
+// itself. (A division per element made the append of a 32K prompt 20% ALU work.)
 struct E4m3Scale {
   float scale, inv;
   bool plain;
@@ -98,22 +102,34 @@ __device__ __forceinline__ E4m3Scale e4m3_scale(float scale) {
   const bool plain = !(scale > 0x1p-60f && scale < 0x1p60f);
   return {scale, __frcp_rn(scale), plain};
 }
-__device__ __forceinline__ float e4m3_quotient(float y, const E4m3Scale& s) {
-  if (s.plain) return __fdiv_rn(y, s.scale);
-  const float q = y * s.inv;
-  const float exact = fmaf(fmaf(-q, s.scale, y), s.inv, q);
-  // q will do where it is zero (the correction would lose the sign of -0), beyond e4m3's
-  // largest, infinite or NaN: one comparison of the bits of |q|, 1024.f = 0x44800000
-  return (__float_as_uint(fabsf(q)) - 1u) < 0x447fffffu ? exact : q;
-}
-__device__ __forceinline__ uint2 pack_e4m3x8(const float* y, const E4m3Scale& s) {
-  uint32_t w[4];
+// 16 quotients as e4m3, two 8-byte chunks
+__device__ __forceinline__ void pack_e4m3x16(const float* y, const E4m3Scale& s, uint2* out0, uint2* out1) {
+  float q[16];
+  float top = 0.f;
+  const float2 inv = make_float2(s.inv, s.inv), scale = make_float2(s.scale, s.scale);
+  const float2 minus_inv = make_float2(-s.inv, -s.inv);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(
-        make_float2(e4m3_quotient(y[2 * i], s), e4m3_quotient(y[2 * i + 1], s)), __NV_SATFINITE,
-        __NV_E4M3);
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  for (int i = 0; i < 16; i += 2) {
+    const float2 v = make_float2(y[i], y[i + 1]);
+    // (a zero of either sign added to a product of that sign leaves it, -0 included, and so
+    // does the order of signs of the remainder)
+    const float2 r = ffma2(v, inv, make_float2(-0.f, -0.f));
+    const float2 rem = ffma2(r, scale, make_float2(-v.x, -v.y));
+    const float2 e = ffma2(rem, minus_inv, r);
+    q[i] = e.x;
+    q[i + 1] = e.y;
+    top = fmax3(top, fabsf(r.x), fabsf(r.y));
+  }
+  if (s.plain || top >= 1024.f) {      // infinite, or far beyond the largest: no correction
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(y[i], s.scale);
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  *out0 = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  *out1 = make_uint2(w[4] | (w[5] << 16), w[6] | (w[7] << 16));
 }
 __device__ __forceinline__ void unpack_bf16x8(uint4 v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -128,13 +144,85 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* f) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// How a thread's two chunks rotate.
+struct RopeLane {
+  int ca, cb;               // their indices in the row
+  bool rot_a, rot_b;        // do they rotate
+  bool interleaved;
+};
+
+// Rows of one tensor, one token, heads h, h + step, ... < heads: x and y point at this
+// thread's first row, xs and ys are bytes from one of its rows to the next. FP8: y is e4m3.
+template <int C, bool ROT, bool FP8>
+__device__ __forceinline__ void rope_rows(const char* x, long long xs, char* y, long long ys, int h,
+                                          int step, int heads, const RopeLane& t, const float2* w,
+                                          const float* scales) {
+  constexpr int U = 4;                       // rows in flight
+  constexpr int kOut = FP8 ? 8 : 16;         // bytes of a stored chunk
+  x += t.ca * 16;
+  y += t.ca * kOut;
+  const int bx = (t.cb - t.ca) * 16, by = (t.cb - t.ca) * kOut;
+#pragma unroll 1
+  for (; h < heads; h += U * step) {
+    uint4 xa[U], xb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u * step < heads) {
+        xa[u] = *reinterpret_cast<const uint4*>(x + u * xs);
+        xb[u] = *reinterpret_cast<const uint4*>(x + u * xs + bx);
+      }
+    x += U * xs;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (h + u * step >= heads) break;
+      if (!FP8 && !ROT) {
+        *reinterpret_cast<uint4*>(y) = xa[u];
+        *reinterpret_cast<uint4*>(y + by) = xb[u];
+      } else {
+        float v[16];
+        unpack_bf16x8(xa[u], v);
+        unpack_bf16x8(xb[u], v + 8);
+        if (ROT) {
+          if (t.interleaved) {               // w is (1, 0) for a chunk that passes through
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x1 = v[2 * i], x2 = v[2 * i + 1];
+              v[2 * i] = x1 * w[i].x - x2 * w[i].y;
+              v[2 * i + 1] = x2 * w[i].x + x1 * w[i].y;
+            }
+          } else {                           // chunk cb holds the partners of chunk ca
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x1 = v[i], x2 = v[8 + i];
+              v[i] = x1 * w[i].x - x2 * w[i].y;
+              v[8 + i] = x2 * w[i].x + x1 * w[i].y;
+            }
+          }
+        }
+        if (FP8) {
+          uint2 a, b;
+          // what passes through is not turned by (1, 0): that would make NaN of infinities
+          if (ROT && !t.rot_a) unpack_bf16x8(xa[u], v);
+          if (ROT && !t.rot_b) unpack_bf16x8(xb[u], v + 8);
+          pack_e4m3x16(v, e4m3_scale(__ldg(scales + h + u * step)), &a, &b);
+          *reinterpret_cast<uint2*>(y) = a;
+          *reinterpret_cast<uint2*>(y + by) = b;
+        } else {
+          *reinterpret_cast<uint4*>(y) = t.rot_a ? pack_bf16x8(v) : xa[u];
+          *reinterpret_cast<uint4*>(y + by) = t.rot_b ? pack_bf16x8(v + 8) : xb[u];
+        }
+      }
+      y += ys;
+    }
+  }
+}
+
 // DST: where keys (and values) go. 0: dense rows ko, no values; 1: bf16 pages; 2: e4m3 pages.
 template <int C, bool ROPE, int DST>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, ROPE ? 2 : 4)
 rope_append_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kTpr = C / 16;                  // threads per row
   constexpr int kRows = kRopeThreads / kTpr;    // rows per sweep of the CTA
-  constexpr int kUnroll = 2;
   // (cos, sin) of token t's pairs: 8 pairs of a thread lie C/16 apart; 8 words between tokens
   // keep the tokens of a warp on different banks
   constexpr int kCsRow = C / 2 + 8;
@@ -145,7 +233,6 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
   const int m0 = blockIdx.x << p.tokens_log2;
   const int tid = threadIdx.x;
   int n_tok = min(TT, p.M - m0);                // tokens of this tile
-  int first_slot = 0;
 
   if (DST != 0) {
     int nn = p.M;
@@ -154,14 +241,12 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
       nn = min(max(want, 0), p.M);
       if (want != nn && tid == 0) raise_device_error(kErrInvalid);
     }
+    const int len = __ldg(p.cache.lens + b);
     n_tok = min(n_tok, nn - m0);
     if (n_tok <= 0) return;
-    const int len = __ldg(p.cache.lens + b);
-    first_slot = len - nn + m0;
     if (tid < n_tok) {
-      const int slot = first_slot + tid;
       long long r = -1;
-      if (len >= nn && len <= p.cache.capacity()) r = p.cache.slot_index(b, 0, slot);
+      if (len >= nn && len <= p.cache.capacity()) r = p.cache.slot_index(b, 0, len - nn + m0 + tid);
       if (r < 0) raise_device_error(kErrInvalid);
       dst_row[tid] = r;
     }
@@ -169,11 +254,11 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
     if (p.cache.acc != nullptr || p.cache.ordinal != nullptr) {
       const int seen = p.seen != nullptr ? __ldg(p.seen + b) : len;
       __syncthreads();
-      for (int i = tid; i < n_tok * p.cache.Hkv; i += kRopeThreads) {
-        const int h = i / n_tok, t = i - h * n_tok;
-        const long long r = dst_row[t];
+      for (int i = tid; i < p.cache.Hkv << p.tokens_log2; i += kRopeThreads) {
+        const int t = i & (TT - 1);
+        const long long r = t < n_tok ? dst_row[t] : -1;
         if (r < 0) continue;
-        const long long at = r + ((long long)h << p.cache.page_log2);
+        const long long at = r + ((long long)(i >> p.tokens_log2) << p.cache.page_log2);
         if (p.cache.acc != nullptr) p.cache.acc[at] = 0.f;
         if (p.cache.ordinal != nullptr) p.cache.ordinal[at] = seen - nn + m0 + t;
       }
@@ -200,103 +285,51 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
   }
   __syncthreads();
 
+  // this thread's row (token and first head) and its two chunks of every row
   const int lane_r = tid / kTpr, t8 = tid % kTpr;
+  const int tok = lane_r & (TT - 1), h0 = lane_r >> p.tokens_log2, step = kRows >> p.tokens_log2;
+  if (tok >= n_tok) return;
   const int rotated = ROPE ? 2 * p.pairs / 8 : 0;     // chunks that rotate (pairs % 8 == 0)
-  // the two 8-element chunks of this thread
-  int ca = t8, cb = t8 + kTpr;
+  RopeLane t;
+  t.ca = t8;
+  t.cb = t8 + kTpr;
   if (ROPE && !p.interleaved && rotated < C / 8) {
     const int hp = rotated / 2;
-    if (t8 < hp) { ca = t8; cb = t8 + hp; }
-    else { ca = rotated + 2 * (t8 - hp); cb = ca + 1; }
+    if (t8 < hp) { t.ca = t8; t.cb = t8 + hp; }
+    else { t.ca = rotated + 2 * (t8 - hp); t.cb = t.ca + 1; }
   }
-  const bool rope_a = ca < rotated, rope_b = cb < rotated;
+  t.rot_a = t.ca < rotated;
+  t.rot_b = t.cb < rotated;
+  t.interleaved = ROPE && p.interleaved;
   float2 w[ROPE ? 8 : 1];
   if (ROPE) {
-    // unused ones (chunks that pass through, tokens behind the tile's last) are never applied
-    const float2* row = cs + (lane_r & (TT - 1)) * kCsRow + t8;
+    const float2* row = cs + tok * kCsRow + t8;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      w[i] = (p.interleaved ? (i < 4 ? rope_a : rope_b) : rope_a) ? row[i * kTpr] : make_float2(1.f, 0.f);
+      w[i] = (t.interleaved && i >= 4 ? t.rot_b : t.rot_a) ? row[i * kTpr] : make_float2(1.f, 0.f);
   }
-  const int nq = p.q.heads, nk = p.k.heads, nv = DST != 0 ? p.v.heads : 0;
-  const int rows = (nq + nk + nv) << p.tokens_log2;
-
-  for (int r0 = lane_r; r0 < rows; r0 += kUnroll * kRows) {
-    uint4 xa[kUnroll], xb[kUnroll];
-    int head[kUnroll], tok[kUnroll];
-    bool live[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * kRows;
-      tok[u] = r & (TT - 1);
-      head[u] = r >> p.tokens_log2;
-      live[u] = r < rows && tok[u] < n_tok;
-      if (live[u]) {
-        const int h = head[u];
-        const HeadsView& src = h < nq ? p.q : (h < nq + nk ? p.k : p.v);
-        const int hh = h < nq ? h : (h < nq + nk ? h - nq : h - nq - nk);
-        const bf16* x = src.data + (long long)b * src.sb + (long long)hh * src.sh +
-                        (long long)(m0 + tok[u]) * src.sm;
-        xa[u] = *reinterpret_cast<const uint4*>(x + ca * 8);
-        xb[u] = *reinterpret_cast<const uint4*>(x + cb * 8);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (!live[u]) continue;
-      const int h = head[u];
-      const bool is_q = h < nq, is_v = h >= nq + nk;
-      float a[8], c[8];
-      const bool raw_copy = DST != 2 || is_q;     // bf16 out: an unrotated chunk stays as it is
-      const bool rot_a = ROPE && !is_v && rope_a, rot_b = ROPE && !is_v && rope_b;
-      if (rot_a || rot_b || !raw_copy) {
-        unpack_bf16x8(xa[u], a);
-        unpack_bf16x8(xb[u], c);
-      }
-      if (ROPE && !is_v) {
-        if (p.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a1 = a[2 * i], a2 = a[2 * i + 1], c1 = c[2 * i], c2 = c[2 * i + 1];
-            a[2 * i] = a1 * w[i].x - a2 * w[i].y;
-            a[2 * i + 1] = a2 * w[i].x + a1 * w[i].y;
-            c[2 * i] = c1 * w[4 + i].x - c2 * w[4 + i].y;
-            c[2 * i + 1] = c2 * w[4 + i].x + c1 * w[4 + i].y;
-          }
-        } else {                     // cb = ca + pairs/8 holds the partners
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x1 = a[i], x2 = c[i];
-            a[i] = x1 * w[i].x - x2 * w[i].y;
-            c[i] = x2 * w[i].x + x1 * w[i].y;
-          }
-        }
-      }
-      if (DST == 0 || is_q) {
-        const HeadsView& dst = is_q ? p.qo : p.ko;
-        const int hh = is_q ? h : h - nq;
-        bf16* y = dst.data + (long long)b * dst.sb + (long long)hh * dst.sh +
-                  (long long)(m0 + tok[u]) * dst.sm;
-        *reinterpret_cast<uint4*>(y + ca * 8) = rot_a ? pack_bf16x8(a) : xa[u];
-        *reinterpret_cast<uint4*>(y + cb * 8) = rot_b ? pack_bf16x8(c) : xb[u];
-      } else {
-        const int hh = is_v ? h - nq - nk : h - nq;
-        const long long r = dst_row[tok[u]];
-        if (r < 0) continue;
-        const long long at = (r + ((long long)hh << p.cache.page_log2)) * C;
-        void* pages = is_v ? p.cache.v_pages : p.cache.k_pages;
-        if (DST == 1) {
-          bf16* y = static_cast<bf16*>(pages) + at;
-          *reinterpret_cast<uint4*>(y + ca * 8) = rot_a ? pack_bf16x8(a) : xa[u];
-          *reinterpret_cast<uint4*>(y + cb * 8) = rot_b ? pack_bf16x8(c) : xb[u];
-        } else {
-          const E4m3Scale sc = e4m3_scale(__ldg((is_v ? p.cache.v_scale : p.cache.k_scale) + hh));
-          uint8_t* y = static_cast<uint8_t*>(pages) + at;
-          *reinterpret_cast<uint2*>(y + ca * 8) = pack_e4m3x8(a, sc);
-          *reinterpret_cast<uint2*>(y + cb * 8) = pack_e4m3x8(c, sc);
-        }
-      }
-    }
+  // this thread's first row of a strided tensor, and the bytes to its next one
+  auto row_of = [&](const HeadsView& v) -> char* {
+    return reinterpret_cast<char*>(v.data + (long long)b * v.sb + (long long)h0 * v.sh +
+                                   (long long)(m0 + tok) * v.sm);
+  };
+  auto step_of = [&](const HeadsView& v) -> long long { return v.sh * step * 2; };
+  if (ROPE)
+    rope_rows<C, true, false>(row_of(p.q), step_of(p.q), row_of(p.qo), step_of(p.qo), h0, step,
+                              p.q.heads, t, w, nullptr);
+  if (DST == 0) {
+    rope_rows<C, true, false>(row_of(p.k), step_of(p.k), row_of(p.ko), step_of(p.ko), h0, step,
+                              p.k.heads, t, w, nullptr);
+  } else {
+    const long long r = dst_row[tok];
+    if (r < 0) return;
+    constexpr int kBytes = C * (DST == 1 ? 2 : 1);
+    const long long at = (r + ((long long)h0 << p.cache.page_log2)) * kBytes;
+    const long long ys = ((long long)step << p.cache.page_log2) * kBytes;
+    rope_rows<C, ROPE, DST == 2>(row_of(p.k), step_of(p.k), static_cast<char*>(p.cache.k_pages) + at,
+                                 ys, h0, step, p.k.heads, t, w, p.cache.k_scale);
+    rope_rows<C, false, DST == 2>(row_of(p.v), step_of(p.v), static_cast<char*>(p.cache.v_pages) + at,
+                                  ys, h0, step, p.v.heads, t, w, p.cache.v_scale);
   }
 }
 
