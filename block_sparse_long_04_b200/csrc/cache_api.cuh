@@ -286,7 +286,9 @@ int launch_decode(const xattn_cache* c, DecodeParams& p, const DecodePlan& d, cu
 // ------------------------------------------------------------------ evict
 struct EvictPlan {
   long long rows, max_moves;
-  size_t off_hole, off_mover, bytes;
+  int cluster, share;           // CTAs per row, most slots of one
+  bool in_smem;                 // a CTA's keys fit its shared memory
+  size_t off_hole, off_mover, off_keys, bytes;
 };
 
 EvictPlan evict_plan(const xattn_cache* c, int budget) {
@@ -297,7 +299,16 @@ EvictPlan evict_plan(const xattn_cache* c, int budget) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   e.off_hole = up((size_t)e.rows * sizeof(int32_t));
   e.off_mover = e.off_hole + up((size_t)(e.rows * e.max_moves) * sizeof(int32_t));
-  e.bytes = e.off_mover + up((size_t)(e.rows * e.max_moves) * sizeof(int32_t));
+  e.off_keys = e.off_mover + up((size_t)(e.rows * e.max_moves) * sizeof(int32_t));
+  // CTAs per row: more while the rows alone leave SMs idle and a part stays worth a
+  // cluster barrier per pass. (8 is the portable most; 16 CTAs, of which few clusters fit
+  // the GPU at once, took 91 us for the eviction of a 128K cache instead of 77.)
+  e.cluster = 1;
+  while (e.cluster < 8 && e.rows * e.cluster * 2 <= 148 && cap / (e.cluster * 2) >= 2048) e.cluster *= 2;
+  e.share = (int)((((cap + e.cluster - 1) / e.cluster) + 3) & ~3ll);
+  e.in_smem = e.share <= kEvMaxKeys;
+  const size_t keys = (size_t)e.rows * e.cluster * (e.share + e.share / 4);
+  e.bytes = e.off_keys + (e.in_smem ? 0 : up(keys * sizeof(uint32_t)));
   return e;
 }
 
@@ -420,31 +431,26 @@ int xattn_cache_evict(const xattn_cache* cache, int budget, int recent, int sink
   p.sink = sink;
   p.C = cache->C;
   p.row_bytes_log2 = ilog2(cache->C * (cache->kv_type == XATTN_KV_BF16 ? 2 : 1));
-  const int cap = cache->max_pages * cache->page;
-  // CTAs per row: more while the rows alone leave SMs idle and a part stays worth a
-  // cluster barrier per pass
-  int cl = 1;
-  while (cl < 8 && e.rows * cl * 2 <= 148 && cap / (cl * 2) >= 2048) cl *= 2;
-  const int share = (((cap + cl - 1) / cl) + 3) & ~3;
-  p.smem_keys = std::min(share, kEvMaxKeys);
+  p.keys = e.in_smem ? nullptr : reinterpret_cast<uint32_t*>(ws + e.off_keys);
+  p.share = e.share;
   static unsigned long long done = 0;
-  if (ensure_smem_limit(evict_select_kernel, kEvMaxKeys * 4, &done) != XATTN_OK) return XATTN_ECUDA;
+  if (ensure_smem_limit(evict_select_kernel, kEvMaxKeys * 5, &done) != XATTN_OK) return XATTN_ECUDA;
   cudaStream_t st = as_stream(stream);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cl, (unsigned)e.rows);
+  cfg.gridDim = dim3(e.cluster, (unsigned)e.rows);
   cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = (size_t)p.smem_keys * 4;
+  cfg.dynamicSmemBytes = e.in_smem ? (size_t)e.share * 5 : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.x = e.cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return XATTN_ECUDA;
   if (e.max_moves == 0) return launch_status();
-  const int per_block = kEvMoveThreads * kEvMoveUnroll >> (p.row_bytes_log2 - 4);   // moves of a sweep
+  const int per_block = kEvMoveThreads >> (p.row_bytes_log2 - 4);     // moves of a sweep
   const long long most = (e.max_moves + per_block - 1) / per_block;
   const long long fill = std::max<long long>(1, 148 * 8 / e.rows);
   return launch_dependent(evict_move_kernel, dim3((unsigned)std::min(most, fill), (unsigned)e.rows),

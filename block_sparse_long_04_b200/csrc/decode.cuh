@@ -660,17 +660,19 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
 // (maximum, sum) of one row over n partials, in log2 units, by one warp: the lanes read
 // the partials side by side, so a row of many costs a few load latencies, not n.
 __device__ __forceinline__ float2 dec_row_stat(const float2* ml, int rows, int n, int lane) {
-  float top = kNegInf, sum = 0.f;
-#pragma unroll 4
-  for (int s = lane; s < n; s += 32) top = fmaxf(top, ml[(long long)s * rows].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float ref = top == kNegInf ? 0.f : top;
-#pragma unroll 4
+  float top = kNegInf, sum = 0.f;       // of this lane's partials
+#pragma unroll 2
   for (int s = lane; s < n; s += 32) {
     const float2 v = ml[(long long)s * rows];
-    sum += ex2(v.x - ref) * v.y;
+    const float up = fmaxf(top, v.x), ref = up == kNegInf ? 0.f : up;
+    sum = sum * ex2(top - ref) + v.y * ex2(v.x - ref);
+    top = up;
   }
+  float all = top;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+  const float ref = all == kNegInf ? 0.f : all;
+  sum *= ex2(top - ref);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return make_float2(ref, sum);
@@ -724,8 +726,8 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
     float y = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) y += ex2(m[u] - st.x) * v[u];
-#pragma unroll 4
-    for (long long s = warp + 4 * U; s < n; s += 4) y += ex2(ml[s * rows].x - st.x) * po[s * rows * C];
+#pragma unroll 2
+    for (int s = warp + 4 * U; s < n; s += 4) y += ex2(ml[(long long)s * rows].x - st.x) * po[(long long)s * rows * C];
     red[tid] = y;
     __syncthreads();
     if (warp == 0) {
@@ -761,7 +763,7 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
     if (at < 0) continue;              // the split kernel raised the error
     const float4 old = *reinterpret_cast<const float4*>(p.cache.acc + at);
     float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 2
     for (int g = 0; g < p.G; ++g) {
       const float4 x = *reinterpret_cast<const float4*>(logits + (long long)g * cap + j);
       const float l = stat[g];

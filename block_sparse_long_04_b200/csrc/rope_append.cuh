@@ -89,40 +89,43 @@ struct RopeParams {
 
 // y / scale for the e4m3 conversion. The quotient must be the correctly rounded one: where it
 // falls on the middle between two e4m3 values, one unit too much or too little turns the
-// result. With r = RN(1/scale), q = RN(y r), the remainder y - q scale is exact in one FMA
-// and RN(q + remainder r) is the rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990),
-// as long as nothing over- or underflows: with scales between 2^-60 and 2^60 that leaves
-// quotients that vanish alike, and large ones. Those, and other scales, take the division
-// itself. (A division per element made the append of a 32K prompt 20% ALU work.)
+// result. With r = RN(1/d), q = RN(x r), the remainder q d - x is exact in one FMA and
+// RN(q - remainder r) is the rounded quotient x / d (Markstein, IBM J. Res. Dev. 34, 1990),
+// as long as nothing over- or underflows. So scale = d 2^k with d in [1, 2), and x = y 2^-k:
+// what that overflows saturates anyway, what it underflows vanishes. (A division per
+// element made the append of a 32K prompt a fifth ALU work, and its code ten times longer.)
 struct E4m3Scale {
-  float scale, inv;
-  bool plain;
+  float d, inv, pow;
 };
 __device__ __forceinline__ E4m3Scale e4m3_scale(float scale) {
-  const bool plain = !(scale > 0x1p-60f && scale < 0x1p60f);
-  return {scale, __frcp_rn(scale), plain};
+  const int k = max((int)(__float_as_uint(scale) >> 23) - 127, -126);   // 2^k; subnormals: 2^-126
+  // 2^-k: normal for k <= 126, and for k = 127 the subnormal 2^-127
+  const float pow = k < 127 ? __uint_as_float((uint32_t)(127 - k) << 23) : __uint_as_float(0x00400000u);
+  const float d = scale * pow;
+  return {d, __frcp_rn(d), pow};
 }
 // 16 quotients as e4m3, two 8-byte chunks
 __device__ __forceinline__ void pack_e4m3x16(const float* y, const E4m3Scale& s, uint2* out0, uint2* out1) {
   float q[16];
   float top = 0.f;
-  const float2 inv = make_float2(s.inv, s.inv), scale = make_float2(s.scale, s.scale);
-  const float2 minus_inv = make_float2(-s.inv, -s.inv);
+  const float2 inv = make_float2(s.inv, s.inv), d = make_float2(s.d, s.d);
+  const float2 minus_inv = make_float2(-s.inv, -s.inv), pow = make_float2(s.pow, s.pow);
+  const float2 zero = make_float2(-0.f, -0.f);      // x + -0 is x, of either sign
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
-    const float2 v = make_float2(y[i], y[i + 1]);
-    // (a zero of either sign added to a product of that sign leaves it, -0 included, and so
-    // does the order of signs of the remainder)
-    const float2 r = ffma2(v, inv, make_float2(-0.f, -0.f));
-    const float2 rem = ffma2(r, scale, make_float2(-v.x, -v.y));
-    const float2 e = ffma2(rem, minus_inv, r);
+    const float2 x = ffma2(make_float2(y[i], y[i + 1]), pow, zero);
+    const float2 r = ffma2(x, inv, zero);
+    const float2 e = ffma2(ffma2(r, d, make_float2(-x.x, -x.y)), minus_inv, r);
     q[i] = e.x;
     q[i + 1] = e.y;
     top = fmax3(top, fabsf(r.x), fabsf(r.y));
   }
-  if (s.plain || top >= 1024.f) {      // infinite, or far beyond the largest: no correction
+  if (top >= 1024.f) {      // far beyond the largest, or infinite (no remainder): saturate
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(y[i], s.scale);
+    for (int i = 0; i < 16; ++i) {
+      const float r = y[i] * s.pow * s.inv;
+      q[i] = fabsf(r) >= 1024.f ? r : q[i];
+    }
   }
   uint32_t w[8];
 #pragma unroll
