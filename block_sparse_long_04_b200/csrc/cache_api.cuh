@@ -14,21 +14,29 @@ inline int ilog2(int v) {
   return n;
 }
 
-// Launches `kern` so that it may start before the kernel ahead of it in the stream has
-// ended; it must begin with grid_dependency_wait().
+// Launches `kern` so that it may be set up before the kernel ahead of it in the stream has
+// ended. Every kernel launched here begins with grid_dependency_wait(), which waits for
+// that kernel (whatever it is) to complete; so stream order holds for all they read and
+// write, and only the launch latency overlaps: about 1 us of a decoding step's 4 to 9 us
+// per call. `cluster` CTAs along x form a cluster.
 template <typename... P, typename... A>
-int launch_dependent(void (*kern)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+int launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster,
+           const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return XATTN_ECUDA;
-  return launch_status();
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? launch_status() : XATTN_ECUDA;
 }
 
 bool page_supported(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
@@ -144,17 +152,10 @@ int launch_rope_append(RopeParams& p, bool rope, int dst, int B, int M, cudaStre
       break;
     }
   const dim3 grid((unsigned)((M + (1LL << p.tokens_log2) - 1) >> p.tokens_log2), (unsigned)B);
-  if (dst == 0)
-    rope_append_kernel<C, true, 0><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (dst == 1 && rope)
-    rope_append_kernel<C, true, 1><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (dst == 1)
-    rope_append_kernel<C, false, 1><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (rope)
-    rope_append_kernel<C, true, 2><<<grid, kRopeThreads, 0, st>>>(p);
-  else
-    rope_append_kernel<C, false, 2><<<grid, kRopeThreads, 0, st>>>(p);
-  return launch_status();
+  auto kern = dst == 0 ? rope_append_kernel<C, true, 0>
+              : dst == 1 ? (rope ? rope_append_kernel<C, true, 1> : rope_append_kernel<C, false, 1>)
+                         : (rope ? rope_append_kernel<C, true, 2> : rope_append_kernel<C, false, 2>);
+  return launch(kern, grid, kRopeThreads, 0, st, 1, p);
 }
 
 int append_common(const xattn_heads* Q, const xattn_heads* K, const xattn_heads* V,
@@ -249,8 +250,7 @@ int launch_decode_split(const CUtensorMap& mk, const CUtensorMap& mv, const Deco
   auto kern = decode_split_kernel<C, FP8, NT>;
   static unsigned long long done = 0;
   if (ensure_smem_limit(kern, L::kSmem, &done) != XATTN_OK) return XATTN_ECUDA;
-  kern<<<148 * L::kPerSm, kDecThreads, L::kSmem, st>>>(mk, mv, p);
-  return launch_status();
+  return launch(kern, dim3(148 * L::kPerSm), kDecThreads, L::kSmem, st, 1, mk, mv, p);
 }
 
 template <int C>
@@ -279,8 +279,8 @@ int launch_decode(const xattn_cache* c, DecodeParams& p, const DecodePlan& d, cu
                              std::max<long long>(1, 148 * 16 / pairs));
   }
   const long long blocks = (long long)c->B * p.Hq * (C / 32) + wb * c->B * c->Hkv;
-  return launch_dependent(decode_join_kernel<C>, dim3((unsigned)blocks), kJoinThreads, st, p, d.rows,
-                          8 * d.NT, (int)wb);
+  return launch(decode_join_kernel<C>, dim3((unsigned)blocks), kJoinThreads, 0, st, 1, p, d.rows,
+                8 * d.NT, (int)wb);
 }
 
 // ------------------------------------------------------------------ evict
@@ -436,25 +436,15 @@ int xattn_cache_evict(const xattn_cache* cache, int budget, int recent, int sink
   static unsigned long long done = 0;
   if (ensure_smem_limit(evict_select_kernel, kEvMaxKeys * 5, &done) != XATTN_OK) return XATTN_ECUDA;
   cudaStream_t st = as_stream(stream);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(e.cluster, (unsigned)e.rows);
-  cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = e.in_smem ? (size_t)e.share * 5 : 0;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = e.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return XATTN_ECUDA;
-  if (e.max_moves == 0) return launch_status();
+  rc = launch(evict_select_kernel, dim3(e.cluster, (unsigned)e.rows), kEvThreads,
+              e.in_smem ? (size_t)e.share * 5 : 0, st, e.cluster, p);
+  if (rc != XATTN_OK) return rc;
+  if (e.max_moves == 0) return XATTN_OK;
   const int per_block = kEvMoveThreads >> (p.row_bytes_log2 - 4);     // moves of a sweep
   const long long most = (e.max_moves + per_block - 1) / per_block;
   const long long fill = std::max<long long>(1, 148 * 8 / e.rows);
-  return launch_dependent(evict_move_kernel, dim3((unsigned)std::min(most, fill), (unsigned)e.rows),
-                          kEvMoveThreads, st, p);
+  return launch(evict_move_kernel, dim3((unsigned)std::min(most, fill), (unsigned)e.rows),
+                kEvMoveThreads, 0, st, 1, p);
 }
 
 }  // extern "C"

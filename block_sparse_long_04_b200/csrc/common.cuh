@@ -42,14 +42,14 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-// Programmatic dependent launch: a kernel launched with that attribute may start while
-// the kernel before it in the stream still runs, and waits here until that one has
-// completed and its writes are visible; the earlier kernel allows the start.
+// Programmatic dependent launch: a kernel launched with that attribute may be set up while
+// the kernel before it in the stream still runs. grid_dependency_wait() waits until that
+// one has completed and its writes are visible (at once if there is none), and must come
+// first in every such kernel. The next kernel may start as this one's blocks exit; an
+// earlier start (griddepcontrol.launch_dependents) gained nothing and, where the waiting
+// blocks took the room of running ones, cost up to a tenth.
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void grid_dependents_may_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // max of three fp32 values in one instruction (sm_100)

@@ -232,7 +232,6 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = p.cache.Hkv * p.HT;
-  grid_dependents_may_start();     // the join's blocks wait for this grid's end themselves
 
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -241,7 +240,10 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
     }
     *abort_flag = 0;
     fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
   }
+  grid_dependency_wait();
   // every warp finds the CTA's share for itself
   const long long total = dec_total<L::kKeys>(p.cache, lane) * per;
   const long long n_cta = total < gridDim.x ? total : gridDim.x;
@@ -258,10 +260,6 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
   if (warp == 4) {
     // ------------------------------------------------------ TMA producer
     const uint32_t part_bytes = (uint32_t)L::kRow << part_log2;
-    if (lane == 0) {
-      prefetch_tmap(&tmK);
-      prefetch_tmap(&tmV);
-    }
     // lane l < n_parts looks up the page of part l, one tile ahead of its load
     auto page_of = [&](const DecPos& q) -> int {
       const int slot = q.tile * L::kKeys + (lane << part_log2);
@@ -681,8 +679,7 @@ __device__ __forceinline__ float2 dec_row_stat(const float2* ml, int rows, int n
 // Blocks [0, B * Hq * C/32): 32 columns of a query head's output, and its lse, from the
 // partials. The others (weights): acc_out[slot] = acc[slot] + sum over the group's heads of
 // the slot's softmax weight, from the logits of the split kernel and the joined statistics.
-// Launched as a programmatic dependent of the split kernel. Its time is a chain of
-// latencies (segment, statistics and values, sum), so the blocks are small, and the values
+// Its time is a chain of latencies (segment, statistics and values, sum), so the blocks are small, and the values
 // are loaded before the statistics that weigh them are known.
 template <int C>
 __global__ void __launch_bounds__(kJoinThreads)

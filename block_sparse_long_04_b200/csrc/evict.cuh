@@ -106,7 +106,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
   __shared__ __align__(8) int2 found[3];    // pass's (digit, candidates before it)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dependents_may_start();              // the moves wait for this grid's end themselves
+  grid_dependency_wait();
   const int CL = gridDim.x;                 // the grid's x is one cluster
   const uint32_t rank = blockIdx.x;
   const int row = blockIdx.y, b = row / p.cache.Hkv, kvh = row - b * p.cache.Hkv;
@@ -337,8 +337,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
 // pool rows, so a move is two dependent loads deep (list, row). Many warps with one move
 // each in flight did better than fewer with two or four (51 against 60 us for the 32768
 // moves of 8 rows each of a 128K cache cut to half: 0.27 GB read and written, 5.2 TB/s;
-// rows of 256 bytes at random places do not reach the copy's 6.5). Launched as a
-// programmatic dependent of the selection.
+// rows of 256 bytes at random places do not reach the copy's 6.5).
 __global__ void __launch_bounds__(kEvMoveThreads)
 evict_move_kernel(const __grid_constant__ EvictParams p) {
   grid_dependency_wait();

@@ -232,6 +232,7 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 cs[ROPE ? kRopeMaxTokens * kCsRow : 1];
   __shared__ long long dst_row[kRopeMaxTokens];   // pool index at head 0, -1: none
 
+  grid_dependency_wait();
   const int b = blockIdx.y, TT = 1 << p.tokens_log2;
   const int m0 = blockIdx.x << p.tokens_log2;
   const int tid = threadIdx.x;
