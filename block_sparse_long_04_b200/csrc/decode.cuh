@@ -46,6 +46,7 @@ constexpr int kDecThreads = 160;      // four MMA warps, one TMA warp
 constexpr int kDecMaxCtas = 444;      // 148 SMs x 3
 constexpr int kJoinThreads = 128;    // four groups of partials x 32 columns
 constexpr int kDecMaxGroup = 128;     // query heads per kv head
+constexpr float kTinyScale = 1e-37f;  // a logit scale that underflows must not make NaN of -inf
 
 struct DecodeParams {
   CacheView cache;
@@ -172,11 +173,10 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two e4m3 (low half of x) -> f16x2, exact
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-  uint32_t r;
-  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(x));
-  return r;
+// four e4m3 -> two f16x2, exact
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t x, uint32_t* lo, uint32_t* hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n" : "=r"(*lo), "=r"(*hi) : "r"(x));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -322,11 +322,27 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
     r0[u] = k0[u] & ((1 << part_log2) - 1);
     part_off[u] = (uint32_t)part[u] * ((uint32_t)L::kRow << part_log2);
   }
-  // shared address of 16-byte chunk `cb` of key row `r` (the TMA swizzle)
+  // Shared-memory places (the TMA swizzle): 16-byte chunk c of row r of a part lies at chunk
+  // place c ^ (r & 7) of its 128-byte row (bf16 rows of 128: in the second half's rows from
+  // c = 8 on), or c ^ ((r / 2) & 3) of its 64-byte row.
   auto chunk = [&](uint32_t base, int r, int cb) -> uint32_t {
     if (L::kRow == 64) return base + r * 64 + ((cb ^ ((r >> 1) & 3)) << 4);
     const uint32_t half = (uint32_t)(cb >> 3) << (7 + part_log2);
     return base + half + r * 128 + (((cb & 7) ^ (r & 7)) << 4);
+  };
+  // ldmatrix reads chunks k and k+1 of a row, k even: with the row's chunk (lane bit) placed
+  // once, the place of any k is one exclusive or away (rows begin at multiples of their size)
+  const int row_a = (((lane >> 3) & 1) << 3) + (lane & 7);     // matrices: rows, then chunks
+  const int row_v = FP8 ? row_a : ((lane >> 4) << 3) + (lane & 7);   // (bf16 V: chunks, rows)
+  uint32_t off_k[SETS], off_v[SETS];
+#pragma unroll
+  for (int u = 0; u < SETS; ++u) {
+    off_k[u] = chunk(part_off[u], r0[u] + row_a, lane >> 4);
+    off_v[u] = L::kTile + chunk(part_off[u], r0[u] + row_v, FP8 ? lane >> 4 : (lane >> 3) & 1);
+  }
+  const uint32_t half_off = 128u << part_log2;
+  auto place = [&](uint32_t row_chunk, int k) -> uint32_t {    // k: a constant
+    return (row_chunk ^ (uint32_t)((k & (L::kRow == 64 ? 3 : 7)) << 4)) + (k >= 8 ? half_off : 0u);
   };
 
   bool ok = true;
@@ -353,7 +369,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
           qb[t][s][0] = h < heads ? *reinterpret_cast<const uint32_t*>(q + s * 16 + i4 * 2) : 0u;
           qb[t][s][1] = h < heads ? *reinterpret_cast<const uint32_t*>(q + s * 16 + i4 * 2 + 8) : 0u;
         }
-        mult[t][0] = mult[t][1] = p.scale_log2;
+        mult[t][0] = mult[t][1] = fmaxf(p.scale_log2, kTinyScale);
       } else {
         // four neighbouring elements per lane and step: the order in which e4m3 pairs
         // come out of a widened key row
@@ -379,7 +395,8 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
           for (int w = 0; w < 2; ++w)
             qb[t][s][w] = pack_f16x2(__uint_as_float(qb[t][s][w] << 16) * down,
                                      __uint_as_float(qb[t][s][w] & 0xffff0000u) * down);
-        const float back = p.scale_log2 * __ldg(p.cache.k_scale + kvh) * __uint_as_float((uint32_t)(127 + e) << 23);
+        const float back = fmaxf(p.scale_log2 * __ldg(p.cache.k_scale + kvh) *
+                                     __uint_as_float((uint32_t)(127 + e) << 23), kTinyScale);
         mult[t][0] = __shfl_sync(0xffffffffu, back, i4 * 8);
         mult[t][1] = __shfl_sync(0xffffffffu, back, i4 * 8 + 4);
       }
@@ -426,22 +443,21 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
         for (int u = 0; u < SETS; ++u)
 #pragma unroll
           for (int t = 0; t < NT; ++t) sc[u][t][0] = sc[u][t][1] = sc[u][t][2] = sc[u][t][3] = 0.f;
-        const int row_a = (((lane >> 3) & 1) << 3) + (lane & 7);   // matrices: rows, then chunks
 #pragma unroll
         for (int k = 0; k < kSteps; k += FP8 ? 2 : 1) {
 #pragma unroll
           for (int u = 0; u < SETS; ++u) {
             uint32_t r[4];
-            ldsm4(r, chunk(stage + part_off[u], r0[u] + row_a, (FP8 ? k : 2 * k) + (lane >> 4)));
+            ldsm4(r, place(stage + off_k[u], FP8 ? k : 2 * k));
             if (!FP8) {
 #pragma unroll
               for (int t = 0; t < NT; ++t) mma16816<false>(sc[u][t], r, qb[t][k][0], qb[t][k][1]);
             } else {
 #pragma unroll
               for (int v = 0; v < 2; ++v) {
-                const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * v]), e4m3x2_to_f16x2(r[2 * v + 1]),
-                                       e4m3x2_to_f16x2(r[2 * v] >> 16),
-                                       e4m3x2_to_f16x2(r[2 * v + 1] >> 16)};
+                uint32_t a[4];
+                e4m3x4_to_f16x2(r[2 * v], &a[0], &a[2]);
+                e4m3x4_to_f16x2(r[2 * v + 1], &a[1], &a[3]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                   mma16816<true>(sc[u][t], a, qb[t][k + v][0], qb[t][k + v][1]);
@@ -456,25 +472,29 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
           float x[SETS][4], mx[2] = {kNegInf, kNegInf};
 #pragma unroll
           for (int u = 0; u < SETS; ++u) {
+            if (least < 16) {       // (mult > 0, so a product of -inf stays -inf)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[u][e] = sc[u][t][e] * mult[t][e & 1];
-              if (least < 16 && hr + 8 * (e >> 1) >= live[u]) x[u][e] = kNegInf;
-              mx[e & 1] = fmaxf(mx[e & 1], x[u][e]);
+              for (int e = 0; e < 4; ++e)
+                if (hr + 8 * (e >> 1) >= live[u]) sc[u][t][e] = kNegInf;
             }
+            mx[0] = fmax3(mx[0], sc[u][t][0], sc[u][t][2]);
+            mx[1] = fmax3(mx[1], sc[u][t][1], sc[u][t][3]);
             if (p.logits != nullptr) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int h = i4 * 2 + (e & 1) + 8 * t, j = hr + 8 * (e >> 1);
                 if (h < heads && j < live[u])
-                  p.logits[((long long)at.b * p.Hq + h0 + h) * p.cache.capacity() + t_first + k0[u] + j] = x[u][e];
+                  p.logits[((long long)at.b * p.Hq + h0 + h) * p.cache.capacity() + t_first + k0[u] + j] =
+                      sc[u][t][e] * mult[t][e & 1];
               }
             }
           }
 #pragma unroll
-          for (int d = 0; d < 2; ++d)
+          for (int d = 0; d < 2; ++d) {
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) mx[d] = fmaxf(mx[d], __shfl_xor_sync(0xffffffffu, mx[d], w));
+            mx[d] *= mult[t][d];
+          }
           // the reference follows a head's maximum only when that has outgrown it by 2^8:
           // the weights stay below 2^8 and a rescaling of O becomes rare
           const bool grow[2] = {mx[0] > m[t][0] + 8.f, mx[1] > m[t][1] + 8.f};
@@ -494,10 +514,9 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
           const float ref[2] = {m[t][0] == kNegInf ? 0.f : m[t][0], m[t][1] == kNegInf ? 0.f : m[t][1]};
 #pragma unroll
           for (int u = 0; u < SETS; ++u) {
-            // one rounding between the logit and the exponential: the product again, fused
+            // the product fused with the difference: one rounding ahead of the exponential
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[u][e] = x[u][e] == kNegInf ? 0.f : ex2(fmaf(sc[u][t][e], mult[t][e & 1], -ref[e & 1]));
+            for (int e = 0; e < 4; ++e) x[u][e] = ex2(fmaf(sc[u][t][e], mult[t][e & 1], -ref[e & 1]));
             l[t][0] += x[u][0] + x[u][2];
             l[t][1] += x[u][1] + x[u][3];
 #pragma unroll
@@ -513,13 +532,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
         // O^T += V^T P^T
 #pragma unroll
         for (int u = 0; u < SETS; ++u) {
-          const uint32_t sV = stage + L::kTile + part_off[u];
           if (!FP8) {
-            const int row_v = ((lane >> 4) << 3) + (lane & 7);
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
               uint32_t a[4];
-              ldsm4t(a, chunk(sV, r0[u] + row_v, 2 * k + ((lane >> 3) & 1)));
+              ldsm4t(a, place(stage + off_v[u], 2 * k));
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 mma16816<false>(o[t][k], a, pb[u][t][0], pb[u][t][1]);
@@ -530,15 +547,14 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
             for (int k = 0; k < kSteps; k += 2) {
               uint32_t r[4];
-              ldsm4t(r, chunk(sV, r0[u] + row_a, k + (lane >> 4)));
+              ldsm4t(r, place(stage + off_v[u], k));
 #pragma unroll
               for (int v = 0; v < 2; ++v) {
                 // a register holds columns (2n, 2n+1) of two keys: regroup by column; the
                 // MMA's rows 0-7 take the even columns, rows 8-15 the odd ones
-                const uint32_t lo = __byte_perm(r[2 * v], 0, 0x3120);
-                const uint32_t hi = __byte_perm(r[2 * v + 1], 0, 0x3120);
-                const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16),
-                                       e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
+                uint32_t a[4];
+                e4m3x4_to_f16x2(__byte_perm(r[2 * v], 0, 0x3120), &a[0], &a[1]);
+                e4m3x4_to_f16x2(__byte_perm(r[2 * v + 1], 0, 0x3120), &a[2], &a[3]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                   mma16816<true>(o[t][k + v], a, pb[u][t][0], pb[u][t][1]);
