@@ -264,8 +264,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
     auto page_of = [&](const DecPos& q) -> int {
       const int slot = q.tile * L::kKeys + (lane << part_log2);
       if (lane >= n_parts || slot >= p.cache.length(q.b)) return -1;
-      return __ldg(p.cache.page_table + (long long)q.b * p.cache.max_pages +
-                   (slot >> p.cache.page_log2));
+      return p.cache.page_table[(long long)q.b * p.cache.max_pages + (slot >> p.cache.page_log2)];
     };
     auto advance = [&](DecPos& q) {
       if (++q.tile == q.tiles) dec_next_item<L::kKeys>(p.cache, q, per);
@@ -395,7 +394,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
           for (int w = 0; w < 2; ++w)
             qb[t][s][w] = pack_f16x2(__uint_as_float(qb[t][s][w] << 16) * down,
                                      __uint_as_float(qb[t][s][w] & 0xffff0000u) * down);
-        const float back = fmaxf(p.scale_log2 * __ldg(p.cache.k_scale + kvh) *
+        const float back = fmaxf(p.scale_log2 * p.cache.k_scale[kvh] *
                                      __uint_as_float((uint32_t)(127 + e) << 23), kTinyScale);
         mult[t][0] = __shfl_sync(0xffffffffu, back, i4 * 8);
         mult[t][1] = __shfl_sync(0xffffffffu, back, i4 * 8 + 4);
@@ -625,7 +624,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
         bar_mma_warps();
       }
       if (g < heads) {
-        const float vs = FP8 ? __ldg(p.cache.v_scale + kvh) : 1.f;
+        const float vs = FP8 ? p.cache.v_scale[kvh] : 1.f;
         const float inv = whole ? vs / sum : vs;
         const float* x0 = xo + row * L::kXRow + c0;
         const float* x1 = x0 + 8 * L::kXRow;

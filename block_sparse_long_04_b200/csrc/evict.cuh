@@ -146,7 +146,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
   *reinterpret_cast<int2*>(&total[1][tid * 2]) = make_int2(0, 0);
   if (CL > 1) cluster_arrive();
 
-  const int seen = p.seen != nullptr ? __ldg(p.seen + b) : len;
+  const int seen = p.seen != nullptr ? p.seen[b] : len;
   const int safe_from = (long long)seen - p.recent < -2147483647ll ? -2147483647 : seen - p.recent;
   // keys of this warp's run, and the pool row of every fourth slot, in shared memory or in
   // the workspace: written and read by the warp alone

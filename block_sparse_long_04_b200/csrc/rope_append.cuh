@@ -48,19 +48,20 @@ struct CacheView {
   int B, Hkv, page_log2, num_pages, max_pages;
 
   __device__ __forceinline__ int capacity() const { return max_pages << page_log2; }
-  // length of sequence b, clamped to what its table can name
-  __device__ __forceinline__ int length(int b) const {
-    const int n = __ldg(lens + b);
-    return n < 0 ? 0 : min(n, capacity());
-  }
+  // Plain loads throughout: the read-only path must not be used for what an earlier kernel
+  // wrote while this one was already being set up (see grid_dependency_wait).
   __device__ __forceinline__ bool length_valid(int b) const {
-    const int n = __ldg(lens + b);
-    return n >= 0 && n <= capacity();
+    return lens[b] >= 0 && lens[b] <= capacity();
+  }
+  // slots of sequence b; 0 for a length that its table cannot hold
+  __device__ __forceinline__ int length(int b) const {
+    const int n = lens[b];
+    return n <= capacity() ? max(n, 0) : 0;
   }
   // index of (slot, kv head) in a [num_pages, Hkv, page] pool, -1 for a bad page id;
   // the slot must lie in [0, capacity)
   __device__ __forceinline__ long long slot_index(int b, int kvh, int slot) const {
-    const int pid = __ldg(page_table + (long long)b * max_pages + (slot >> page_log2));
+    const int pid = page_table[(long long)b * max_pages + (slot >> page_log2)];
     if (pid < 0 || pid >= num_pages) return -1;
     return ((((long long)pid * Hkv + kvh) << page_log2) + (slot & ((1 << page_log2) - 1)));
   }
@@ -207,7 +208,7 @@ __device__ __forceinline__ void rope_rows(const char* x, long long xs, char* y, 
           // what passes through is not turned by (1, 0): that would make NaN of infinities
           if (ROT && !t.rot_a) unpack_bf16x8(xa[u], v);
           if (ROT && !t.rot_b) unpack_bf16x8(xb[u], v + 8);
-          pack_e4m3x16(v, e4m3_scale(__ldg(scales + h + u * step)), &a, &b);
+          pack_e4m3x16(v, e4m3_scale(scales[h + u * step]), &a, &b);
           *reinterpret_cast<uint2*>(y) = a;
           *reinterpret_cast<uint2*>(y + by) = b;
         } else {
@@ -239,24 +240,22 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
   int n_tok = min(TT, p.M - m0);                // tokens of this tile
 
   if (DST != 0) {
-    int nn = p.M;
-    if (p.n_new != nullptr) {
-      const int want = __ldg(p.n_new + b);
-      nn = min(max(want, 0), p.M);
-      if (want != nn && tid == 0) raise_device_error(kErrInvalid);
+    const int nn = p.n_new != nullptr ? p.n_new[b] : p.M;
+    const int len = p.cache.lens[b];
+    if (nn < 0 || nn > p.M || nn > len || len > p.cache.capacity()) {
+      if (tid == 0) raise_device_error(kErrInvalid);
+      return;
     }
-    const int len = __ldg(p.cache.lens + b);
     n_tok = min(n_tok, nn - m0);
     if (n_tok <= 0) return;
     if (tid < n_tok) {
-      long long r = -1;
-      if (len >= nn && len <= p.cache.capacity()) r = p.cache.slot_index(b, 0, len - nn + m0 + tid);
+      const long long r = p.cache.slot_index(b, 0, len - nn + m0 + tid);
       if (r < 0) raise_device_error(kErrInvalid);
       dst_row[tid] = r;
     }
     // new slots: no weight yet, and the token's index in its sequence
     if (p.cache.acc != nullptr || p.cache.ordinal != nullptr) {
-      const int seen = p.seen != nullptr ? __ldg(p.seen + b) : len;
+      const int seen = p.seen != nullptr ? p.seen[b] : len;
       __syncthreads();
       for (int i = tid; i < p.cache.Hkv << p.tokens_log2; i += kRopeThreads) {
         const int t = i & (TT - 1);
@@ -275,7 +274,7 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
       const int t = i / P, pr = i - t * P;
       const int ax = (pr >= p.end0) + (pr >= p.end1) + (pr >= p.end2);
       // turns = pos * inv_freq / (2 pi), then its fraction in [-1/2, 1/2]
-      const double turns = (double)__ldg(pos + t * p.axes + ax) * __ldg(p.inv_freq + pr) *
+      const double turns = (double)pos[t * p.axes + ax] * p.inv_freq[pr] *
                            0.15915494309189533577;
       const float half_turns = (float)(2.0 * (turns - rint(turns)));
       float s, c;

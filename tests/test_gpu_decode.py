@@ -693,6 +693,53 @@ def test_on_a_side_stream_and_in_graphs():
         assert same_cache(s[0], new[0])
 
 
+def test_steps_without_a_pause_equal_steps_with_one():
+    """Lengths, pages and queries change between calls that nothing waits for; the same steps
+    with a synchronisation after every call give the same bits. (The calls overlap their
+    set-up with the work ahead of them; what they read must not be from before it.)"""
+    B, Hq, Hkv, C, page, steps = 3, 8, 2, 64, 16, 40
+    rot = xa.Rotary.make((32,))
+    g = torch.Generator().manual_seed(4)
+    xs = torch.randn(steps, B, 1, Hq + 2 * Hkv, C, generator=g).bfloat16().cuda()
+    start = make_cache(8, [40, 3, 0], Hkv, C, page, slack=3, spare=40)
+    free = [p for p in range(start.num_pages) if p not in set(start.page_table.flatten().tolist())]
+    fresh = torch.tensor(free, dtype=torch.int32).cuda()
+
+    def go(pause):
+        c = clone_cache(start)
+        seen, taken, out = c.lens.clone(), 0, []
+        ws = torch.empty(xa.xattn_decode_workspace_size(c, Hq, True), dtype=torch.uint8, device="cuda")
+        ews = torch.empty(xa.xattn_cache_evict_workspace_size(c, 44), dtype=torch.uint8, device="cuda")
+        lens = [40, 3, 0]
+        for i in range(steps):
+            for b in range(B):
+                if lens[b] % page == 0 and lens[b] // page >= -(-[40, 3, 0][b] // page) \
+                        and int(start.page_table[b, lens[b] // page]) < 0:
+                    c.page_table[b, lens[b] // page].copy_(fresh[taken])
+                    taken += 1
+                lens[b] += 1
+            c.lens.add_(1)
+            seen.add_(1)
+            q, k, v = (t.transpose(1, 2) for t in xs[i].split([Hq, Hkv, Hkv], 2))
+            qo, o, lse = torch.empty_like(q.contiguous()), torch.empty(B, Hq, 1, C, dtype=torch.bfloat16,
+                                                                       device="cuda"), torch.empty(B, Hq, device="cuda")
+            for call in (lambda: xa.xattn_rope_append(q, k, v, (seen - 1).view(B, 1, 1), rot, c, qo, seen=seen),
+                         lambda: xa.xattn_decode_attn(qo, c, 0.125, o, ws, lse=lse, weights=True),
+                         lambda: xa.xattn_cache_evict(c, 44, ews, recent=8, seen=seen)):
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+            c.lens.clamp_(max=44)
+            lens = [min(n, 44) for n in lens]
+            out += [o.clone(), lse.clone()]
+        return c, out
+
+    (a, oa), (b, ob) = go(False), go(True)
+    assert all(torch.equal(x, y) for x, y in zip(oa, ob))
+    assert same_cache(a, b) and torch.equal(a.lens, b.lens)
+    assert not any(torch.isnan(x).any() for x in oa)
+
+
 def test_pool_beyond_32_bit_offsets():
     """Pages whose element offsets pass 2^31 (and byte offsets 2^32): append, decode and
     evict there give what they give in a small pool."""
@@ -759,10 +806,18 @@ def test_bad_lengths_and_counts_touch_nothing_and_raise():
     cap = c.max_pages * c.page
     before = clone_cache(c)
     q = torch.randn(2, 4, C, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    good, _ = run_decode(c, q, 0.1)
     for n in (-1, cap + 1, 2 ** 31 - 1, -2 ** 31):
         c.lens[0] = n
-        run_decode(c, q, 0.1)
+        o, lse = run_decode(c, q, 0.1)
         assert _error() == xa.XATTN_EINVAL
+        assert (o[0] == 0).all() and torch.isneginf(lse[0]).all() and torch.equal(o[1], good[1])
+        c2 = clone_cache(c)
+        c2.lens[1] = 5                                # below the budget: nothing may move
+        ws = poisoned(xa.xattn_cache_evict_workspace_size(c, 20), torch.uint8)
+        xa.xattn_cache_evict(c2, 20, ws, recent=2)
+        assert _error() == xa.XATTN_EINVAL
+        assert same_cache(c2, c)
         kv = torch.zeros(2, 2, 2, 3, C).bfloat16().cuda()
         c2 = clone_cache(c)
         xa.xattn_cache_append(kv[0], kv[1], c2, n_new=torch.tensor([3, 0], dtype=torch.int32).cuda())
@@ -770,10 +825,11 @@ def test_bad_lengths_and_counts_touch_nothing_and_raise():
         assert same_cache(c2, c)
     c = clone_cache(before)
     kv = torch.ones(2, 2, 2, 3, C).bfloat16().cuda()
-    for new in ([-1, 0], [4, 0]):                     # outside [0, T]; 4 is taken as 3
+    for new in ([-1, 0], [4, 0]):                     # outside [0, T]
         c2 = clone_cache(c)
         xa.xattn_cache_append(kv[0], kv[1], c2, n_new=torch.tensor(new, dtype=torch.int32).cuda())
         assert _error() == xa.XATTN_EINVAL
+        assert same_cache(c2, c)
     c.lens[0] = 2                                     # more new tokens than slots
     c2 = clone_cache(c)
     xa.xattn_cache_append(kv[0], kv[1], c2, n_new=torch.tensor([3, 0], dtype=torch.int32).cuda())
