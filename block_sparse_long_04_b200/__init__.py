@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -56,7 +57,9 @@ SIGNATURES = {
                                 _P, _P, _Z, _P]),
 }
 
-# structs of the decoding operators; fields mirror include/xattn.h
+# Structs of the decoding operators; fields mirror include/xattn.h. The wrappers pass them
+# as packed bytes (made in a tenth of a ctypes.Structure's time: a decoding step is a few
+# microseconds of GPU time, so the host's count); the classes name the layout.
 class _Heads(ctypes.Structure):
     _fields_ = [("data", _P), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
                 ("stride_m", ctypes.c_longlong), ("heads", _I)]
@@ -73,15 +76,19 @@ class _Cache(ctypes.Structure):
                 ("C", _I), ("page", _I), ("num_pages", _I), ("max_pages", _I), ("kv_type", _I)]
 
 
-_PH, _PR, _PC = (ctypes.POINTER(t) for t in (_Heads, _Rotary, _Cache))
+_pack_heads = struct.Struct("Pqqqi4x").pack
+_pack_rotary = struct.Struct("PP4iiii4x").pack
+_pack_cache = struct.Struct("8P7i4x").pack
+
+_S = ctypes.c_char_p     # a packed struct
 SIGNATURES.update({
-    "xattn_rope": (_I, [_PH, _PH, _PR, _I, _I, _I, _I, _PH, _PH, _P]),
-    "xattn_cache_append": (_I, [_PH, _PH, _PC, _I, _P, _P, _P]),
-    "xattn_rope_append": (_I, [_PH, _PH, _PH, _PR, _PC, _I, _P, _P, _PH, _P]),
-    "xattn_decode_workspace_size": (_Z, [_PC, _I, _I]),
-    "xattn_decode_attn": (_I, [_PH, _PC, _F, _P, _P, _P, _P, _Z, _P]),
-    "xattn_cache_evict_workspace_size": (_Z, [_PC, _I]),
-    "xattn_cache_evict": (_I, [_PC, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
+    "xattn_rope": (_I, [_S, _S, _S, _I, _I, _I, _I, _S, _S, _P]),
+    "xattn_cache_append": (_I, [_S, _S, _S, _I, _P, _P, _P]),
+    "xattn_rope_append": (_I, [_S, _S, _S, _S, _S, _I, _P, _P, _S, _P]),
+    "xattn_decode_workspace_size": (_Z, [_S, _I, _I]),
+    "xattn_decode_attn": (_I, [_S, _S, _F, _P, _P, _P, _P, _Z, _P]),
+    "xattn_cache_evict_workspace_size": (_Z, [_S, _I]),
+    "xattn_cache_evict": (_I, [_S, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
 })
 
 XATTN_KV_BF16, XATTN_KV_E4M3 = 0, 1
@@ -411,10 +418,10 @@ def _device_of(*ts) -> int:
 
 def _call(fn, dev: int, stream, *args) -> None:
     """Calls a C entry point on `stream` (default: the current one of device `dev`), with
-    `dev` the current device. A decoding step is a few microseconds of GPU time, so this
-    path avoids the objects that torch.cuda.current_stream() and .device would make."""
+    `dev` the current device. (The raw getters avoid the objects that
+    torch.cuda.current_stream() and torch.device make.)"""
     st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -423,8 +430,8 @@ def _call(fn, dev: int, stream, *args) -> None:
         raise XAttnError(rc, fn.__name__)
 
 
-def _heads(t: torch.Tensor, what: str, shape=None) -> _Heads:
-    """[B, H, M, C] bf16 rows at any strides with contiguous elements."""
+def _heads(t: torch.Tensor, what: str, shape=None) -> bytes:
+    """[B, H, M, C] bf16 rows at any strides with contiguous elements, as an xattn_heads."""
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{what} must be bfloat16")
     size = t.shape
@@ -436,7 +443,13 @@ def _heads(t: torch.Tensor, what: str, shape=None) -> _Heads:
     if sc != 1 and C > 1:
         raise ValueError(f"the elements of a row of {what} must be contiguous")
     # the stride of a dimension of size 1 means nothing and need not be aligned
-    return _Heads(t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, sm if M > 1 else 0, H)
+    return _pack_heads(t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, sm if M > 1 else 0, H)
+
+
+def _workspace(t) -> tuple:
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _want(t, what: str, dtype, shape) -> None:
@@ -463,7 +476,7 @@ class Rotary:
         _want(inv_freq, "inv_freq", torch.float64, (sum(sections),))
         _device_of(inv_freq)
         self.inv_freq, self.sections, self.interleaved = inv_freq, sections, bool(interleaved)
-        self._sections = (_I * 4)(*sections)
+        self._sections = sections + (0,) * (XATTN_ROPE_MAX_AXES - len(sections))
 
     @staticmethod
     def make(sections, base: float = 10000.0, interleaved: bool = False, device="cuda") -> "Rotary":
@@ -471,15 +484,12 @@ class Rotary:
         f = [base ** (-torch.arange(n, dtype=torch.float64) / n) for n in sections if n]
         return Rotary(torch.cat(f).to(device), sections, interleaved)
 
-    def _struct(self, pos: torch.Tensor, B: int, M: int) -> _Rotary:
-        if pos.dim() == 2:
-            _want(pos, "pos", torch.int32, (M, len(self.sections)))
-            n = 1
-        else:
-            _want(pos, "pos", torch.int32, (B, M, len(self.sections)))
-            n = B
-        return _Rotary(pos.data_ptr(), self.inv_freq.data_ptr(), self._sections, len(self.sections),
-                       int(self.interleaved), n)
+    def _struct(self, pos: torch.Tensor, B: int, M: int) -> bytes:
+        axes = len(self.sections)
+        shared = pos.dim() == 2
+        _want(pos, "pos", torch.int32, (M, axes) if shared else (B, M, axes))
+        return _pack_rotary(pos.data_ptr(), self.inv_freq.data_ptr(), *self._sections, axes,
+                            self.interleaved, 1 if shared else B)
 
 
 class PagedCache:
@@ -521,8 +531,7 @@ class PagedCache:
         self.B, self.Hkv, self.C, self.page = B, Hkv, C, page
         self.num_pages, self.max_pages = P, max_pages
         self.kv_type = XATTN_KV_E4M3 if e4m3 else XATTN_KV_BF16
-        self._c = _Cache(B=B, Hkv=Hkv, C=C, page=page, num_pages=P, max_pages=max_pages,
-                         kv_type=self.kv_type)
+        self._shape = (B, Hkv, C, page, P, max_pages, self.kv_type)
         self._checked = True
 
     def __setattr__(self, name, value):
@@ -550,14 +559,11 @@ class PagedCache:
             torch.zeros(pool, dtype=torch.float32, device=dev) if eviction else None,
             torch.zeros(pool, dtype=torch.int32, device=dev) if eviction else None)
 
-    def _struct(self) -> _Cache:
+    def _struct(self) -> bytes:
         # the shapes are fixed; the addresses are read on every call
-        c = self._c
-        c.k_pages, c.v_pages = self.k_pages.data_ptr(), self.v_pages.data_ptr()
-        c.k_scale, c.v_scale = _ptr(self.k_scale), _ptr(self.v_scale)
-        c.acc, c.ordinal = _ptr(self.acc), _ptr(self.ordinal)
-        c.page_table, c.lens = self.page_table.data_ptr(), self.lens.data_ptr()
-        return c
+        return _pack_cache(self.k_pages.data_ptr(), self.v_pages.data_ptr(), _ptr(self.k_scale) or 0,
+                           _ptr(self.v_scale) or 0, _ptr(self.acc) or 0, _ptr(self.ordinal) or 0,
+                           self.page_table.data_ptr(), self.lens.data_ptr(), *self._shape)
 
 
 def xattn_rope(Q, K, pos, rotary: Rotary, Qo, Ko, inverse: bool = False, stream=None) -> None:
@@ -618,10 +624,21 @@ def xattn_decode_attn(Q, cache: PagedCache, softmax_scale: float, O, workspace, 
     weights adds every slot's softmax weight, summed over the query heads of its KV head,
     to cache.acc, into acc_out (default: cache.acc itself)."""
     dev = _device_of(Q, cache.k_pages, O, workspace, lse, acc_out)
-    q = _heads(Q.unsqueeze(2) if Q.dim() == 3 else Q, "Q", (cache.B, Q.shape[1], 1, cache.C))
-    _want(O, "O", torch.bfloat16, Q.shape)
+    shape = Q.shape
+    if len(shape) == 3:
+        B, H, C = shape
+        sb, sh, sc = Q.stride()
+        if Q.dtype is not torch.bfloat16:
+            raise TypeError("Q must be bfloat16")
+        if B != cache.B or C != cache.C or sc != 1:
+            raise ValueError(f"Q has shape {tuple(shape)}, [{cache.B}, Hq, {cache.C}] with contiguous rows "
+                             "is wanted")
+        q = _pack_heads(Q.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, 0, H)
+    else:
+        q = _heads(Q, "Q", (cache.B, shape[1], 1, cache.C))
+    _want(O, "O", torch.bfloat16, shape)
     if lse is not None:
-        _want(lse, "lse", torch.float32, (cache.B, Q.shape[1]))
+        _want(lse, "lse", torch.float32, (cache.B, shape[1]))
     if weights:
         if cache.acc is None:
             raise ValueError("weights need a cache with acc")
@@ -631,10 +648,8 @@ def xattn_decode_attn(Q, cache: PagedCache, softmax_scale: float, O, workspace, 
             _want(acc_out, "acc_out", torch.float32, cache.acc.shape)
     elif acc_out is not None:
         raise ValueError("acc_out needs weights=True")
-    _want(workspace, "workspace", workspace.dtype, workspace.shape)
     _call(_lib.xattn_decode_attn, dev, stream, q, cache._struct(), float(softmax_scale), O.data_ptr(),
-          _ptr(lse), _ptr(acc_out), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+          _ptr(lse), _ptr(acc_out), *_workspace(workspace))
 
 
 def xattn_cache_evict_workspace_size(cache: PagedCache, budget: int) -> int:
@@ -658,7 +673,6 @@ def xattn_cache_evict(cache: PagedCache, budget: int, workspace, recent: int = 0
         ord_out = cache.ordinal
     else:
         _want(ord_out, "ord_out", torch.int32, cache.ordinal.shape)
-    _want(workspace, "workspace", workspace.dtype, workspace.shape)
     _call(_lib.xattn_cache_evict, dev, stream, cache._struct(), int(budget), int(recent), int(sink),
           _per_sequence(seen, "seen", cache.B), acc_out.data_ptr(), ord_out.data_ptr(),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+          *_workspace(workspace))

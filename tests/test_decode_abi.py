@@ -22,16 +22,16 @@ def cache(**kw):
     a = dict(k_pages=FAKE, v_pages=FAKE, k_scale=None, v_scale=None, acc=FAKE, ordinal=FAKE,
              page_table=FAKE, lens=FAKE, B=2, Hkv=2, C=128, page=64, num_pages=10, max_pages=4, kv_type=0)
     a.update(kw)
-    return xa._Cache(*[a[n] for n, _ in xa._Cache._fields_])
+    return bytes(xa._Cache(*[a[n] for n, _ in xa._Cache._fields_]))
 
 
 def heads(H=4, data=FAKE, sb=65536, sh=8192, sm=128):
-    return xa._Heads(data, sb, sh, sm, H)
+    return bytes(xa._Heads(data, sb, sh, sm, H))
 
 
 def rotary(sections=(64,), axes=None, pos=FAKE, inv_freq=FAKE, pos_batch=1, interleaved=0):
     s = (ctypes.c_int * 4)(*sections)
-    return xa._Rotary(pos, inv_freq, s, len(sections) if axes is None else axes, interleaved, pos_batch)
+    return bytes(xa._Rotary(pos, inv_freq, s, len(sections) if axes is None else axes, interleaved, pos_batch))
 
 
 BAD_CACHES = [
@@ -65,6 +65,11 @@ def test_structs_match_the_header(tmp_path, repo_root):
         want.append(ctypes.sizeof(py))
         want += [getattr(py, f).offset for f, _ in py._fields_]
     assert got == want
+    # and the packers write that layout
+    assert xa._pack_heads(1, 2, 3, 4, 5) == bytes(xa._Heads(1, 2, 3, 4, 5))
+    assert xa._pack_rotary(1, 2, 3, 4, 5, 6, 7, True, 9) == \
+        bytes(xa._Rotary(1, 2, (ctypes.c_int * 4)(3, 4, 5, 6), 7, 1, 9))
+    assert xa._pack_cache(*range(15)) == bytes(xa._Cache(*range(15)))
 
 
 # ------------------------------------------------------------------- rope
@@ -237,12 +242,12 @@ def test_binding_checks_tensors():
 
 def test_heads_of_strided_views():
     qkv = torch.zeros(2, 5, 12, 64, dtype=torch.bfloat16)
-    h = xa._heads(qkv[:, :, 8:10].transpose(1, 2), "K")
+    h = xa._Heads.from_buffer_copy(xa._heads(qkv[:, :, 8:10].transpose(1, 2), "K"))
     assert (h.stride_b, h.stride_h, h.stride_m, h.heads) == (5 * 12 * 64, 64, 12 * 64, 2)
     assert h.data == qkv.data_ptr() + 8 * 64 * 2
     # a dimension of size 1 has no stride to speak of
-    assert xa._heads(torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16).as_strided((1, 1, 1, 64), (3, 5, 7, 1)),
-                     "K").stride_b == 0
+    one = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16).as_strided((1, 1, 1, 64), (3, 5, 7, 1))
+    assert xa._Heads.from_buffer_copy(xa._heads(one, "K")).stride_b == 0
     with pytest.raises(ValueError):
         xa._heads(qkv.transpose(2, 3), "K")
     with pytest.raises(TypeError):
