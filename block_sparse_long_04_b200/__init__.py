@@ -676,3 +676,34 @@ def xattn_cache_evict(cache: PagedCache, budget: int, workspace, recent: int = 0
     _call(_lib.xattn_cache_evict, dev, stream, cache._struct(), int(budget), int(recent), int(sink),
           _per_sequence(seen, "seen", cache.B), acc_out.data_ptr(), ord_out.data_ptr(),
           *_workspace(workspace))
+
+
+@dataclass
+class DecodeBuffers:
+    """Device buffers of one layer's decoding step (allocated once, reused)."""
+    Q: torch.Tensor          # rotated queries [B, Hq, 1, C]
+    O: torch.Tensor
+    lse: Optional[torch.Tensor]
+    workspace: torch.Tensor
+
+    @staticmethod
+    def allocate(cache: PagedCache, Hq: int, weights: bool = False, with_lse: bool = False):
+        dev = cache.k_pages.device
+        q = torch.empty((cache.B, Hq, 1, cache.C), dtype=torch.bfloat16, device=dev)
+        return DecodeBuffers(
+            Q=q, O=torch.empty_like(q),
+            lse=torch.empty((cache.B, Hq), dtype=torch.float32, device=dev) if with_lse else None,
+            workspace=torch.empty(max(1, xattn_decode_workspace_size(cache, Hq, weights)),
+                                  dtype=torch.uint8, device=dev))
+
+
+def xattn_decode_step(Q, K, V, pos, rotary: Rotary, cache: PagedCache, bufs: DecodeBuffers, seen=None,
+                      weights: bool = False, softmax_scale: Optional[float] = None,
+                      stream=None) -> torch.Tensor:
+    """One token per sequence through a layer after its prefill: rotate Q and K by pos, append
+    K and V to the cache (cache.lens already counts the token), attend; returns bufs.O.
+    weights accumulates the slots' softmax weights in cache.acc, for xattn_cache_evict."""
+    scale = 1.0 / math.sqrt(cache.C) if softmax_scale is None else softmax_scale
+    xattn_rope_append(Q, K, V, pos, rotary, cache, bufs.Q, seen=seen, stream=stream)
+    xattn_decode_attn(bufs.Q, cache, scale, bufs.O, bufs.workspace, bufs.lse, weights, stream=stream)
+    return bufs.O

@@ -202,11 +202,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 __device__ __forceinline__ void bar_mma_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+// Cached rows are read once per call: first to leave L2, where the partials, logits and
+// queries should stay (128K keys 86.6 -> 84.5 us, ragged e4m3 batch 103.3 -> 100.4 us).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "{\n .reg .b64 once;\n createpolicy.fractional.L2::evict_first.b64 once, 1.0;\n"
+      " cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], once;\n}\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
@@ -757,6 +760,24 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
   const int b = pair / p.cache.Hkv, kvh = pair - b * p.cache.Hkv;
   const int len = p.cache.length(b);
   if (first * (kJoinThreads * 4) >= len) return;
+  const int cap = p.cache.capacity();
+  const float* logits = p.logits + ((long long)b * Hq + kvh * p.G) * cap;
+  // four neighbouring slots per thread (never across a page): 16-byte loads. The first kPre
+  // heads' logits and the old weights are on their way one round ahead, the first round's
+  // while the statistics are worked out.
+  constexpr int kPre = 4;
+  int j = (first * kJoinThreads + tid) * 4;
+  long long at = -1;
+  float4 old, x[kPre];
+  auto load = [&]() {
+    at = j < len ? p.cache.slot_index(b, kvh, j) : -1;
+    if (at < 0) return;                // a bad page: the split kernel raised the error
+    old = *reinterpret_cast<const float4*>(p.cache.acc + at);
+#pragma unroll
+    for (int g = 0; g < kPre; ++g)
+      if (g < p.G) x[g] = *reinterpret_cast<const float4*>(logits + (long long)g * cap + j);
+  };
+  load();
   // base-2 log-sum-exp of every head of the group
   for (int g = warp; g < p.G; g += kJoinThreads / 32) {
     const int item = b * per + kvh * p.HT + g / heads_per_tile;
@@ -767,30 +788,34 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
     if (lane == 0) stat[g] = st.y == 0.f ? -kNegInf : st.x + log2f(st.y);
   }
   __syncthreads();
-  const int cap = p.cache.capacity();
-  const float* logits = p.logits + ((long long)b * Hq + kvh * p.G) * cap;
-  // four neighbouring slots per thread (never across a page): 16-byte loads
-  for (int j = (first * kJoinThreads + tid) * 4; j < len; j += weight_blocks * kJoinThreads * 4) {
-    const long long at = p.cache.slot_index(b, kvh, j);
-    if (at < 0) continue;              // the split kernel raised the error
-    const float4 old = *reinterpret_cast<const float4*>(p.cache.acc + at);
+  while (j < len) {
+    const int j_now = j;
+    const long long at_now = at;
     float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& v, float l) {
+      w.x += ex2(v.x - l);
+      w.y += ex2(v.y - l);
+      w.z += ex2(v.z - l);
+      w.w += ex2(v.w - l);
+    };
+    if (at_now >= 0) {
+#pragma unroll
+      for (int g = 0; g < kPre; ++g)
+        if (g < p.G) add(x[g], stat[g]);
 #pragma unroll 2
-    for (int g = 0; g < p.G; ++g) {
-      const float4 x = *reinterpret_cast<const float4*>(logits + (long long)g * cap + j);
-      const float l = stat[g];
-      w.x += ex2(x.x - l);
-      w.y += ex2(x.y - l);
-      w.z += ex2(x.z - l);
-      w.w += ex2(x.w - l);
+      for (int g = kPre; g < p.G; ++g)
+        add(*reinterpret_cast<const float4*>(logits + (long long)g * cap + j_now), stat[g]);
+      w = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
     }
-    w = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
-    if (j + 4 <= len) {
-      *reinterpret_cast<float4*>(p.acc_out + at) = w;
+    j += weight_blocks * kJoinThreads * 4;
+    load();
+    if (at_now < 0) continue;
+    if (j_now + 4 <= len) {
+      *reinterpret_cast<float4*>(p.acc_out + at_now) = w;
     } else {                           // the slots behind the end stay as they were
-      p.acc_out[at] = w.x;
-      if (j + 1 < len) p.acc_out[at + 1] = w.y;
-      if (j + 2 < len) p.acc_out[at + 2] = w.z;
+      p.acc_out[at_now] = w.x;
+      if (j_now + 1 < len) p.acc_out[at_now + 1] = w.y;
+      if (j_now + 2 < len) p.acc_out[at_now + 2] = w.z;
     }
   }
 }

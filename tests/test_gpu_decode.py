@@ -637,6 +637,26 @@ def test_prefill_append_decode_evict_decode():
                     assert set(range(M + T - 16, M + T)) | set(range(4)) <= left
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_step_is_its_two_calls(e4m3):
+    B, Hq, Hkv, C = 3, 8, 2, 64
+    a = make_cache(6, [40, 1, 16], Hkv, C, 16, e4m3)
+    b = clone_cache(a)
+    x = torch.randn(B, 1, Hq + 2 * Hkv, C, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    q, k, v = (t.transpose(1, 2) for t in x.split([Hq, Hkv, Hkv], 2))
+    rot, pos = xa.Rotary.make((32,)), (a.lens - 1).view(B, 1, 1)
+    bufs = xa.DecodeBuffers.allocate(a, Hq, weights=True, with_lse=True)
+    for t in (bufs.Q, bufs.O, bufs.lse, bufs.workspace):
+        t.view(torch.uint8).fill_(0xFF)
+    o = xa.xattn_decode_step(q, k, v, pos, rot, a, bufs, weights=True)
+    qo = poisoned((B, Hq, 1, C), torch.bfloat16)
+    xa.xattn_rope_append(q, k, v, pos, rot, b, qo)
+    before = f64(b.acc)
+    o2, lse2 = run_decode(b, qo[:, :, 0], 0.125, True)
+    assert torch.equal(o[:, :, 0], o2) and torch.equal(bufs.lse, lse2) and same_cache(a, b)
+    check_decode(b, qo[:, :, 0], 0.125, o2, lse2, before, f64(b.acc))
+
+
 def test_on_a_side_stream_and_in_graphs():
     """A decoding step captured into a graph and replayed with new inputs, lengths and pages,
     next to another graph with a workspace of its own."""
