@@ -278,7 +278,7 @@ int launch_decode(const xattn_cache* c, DecodeParams& p, const DecodePlan& d, cu
     wb = std::min<long long>(((long long)c->max_pages * c->page + kSlots - 1) / kSlots,
                              std::max<long long>(1, 148 * 16 / pairs));
   }
-  const long long blocks = (long long)c->B * p.Hq * (C / 32) + wb * c->B * c->Hkv;
+  const long long blocks = (long long)c->B * p.Hq + wb * c->B * c->Hkv;
   return launch(decode_join_kernel<C>, dim3((unsigned)blocks), kJoinThreads, 0, st, 1, p, d.rows,
                 8 * d.NT, (int)wb);
 }

@@ -44,7 +44,7 @@ namespace xattn {
 
 constexpr int kDecThreads = 160;      // four MMA warps, one TMA warp
 constexpr int kDecMaxCtas = 444;      // 148 SMs x 3
-constexpr int kJoinThreads = 128;    // four groups of partials x 32 columns
+constexpr int kJoinThreads = 128;     // at least the largest C
 constexpr int kDecMaxGroup = 128;     // query heads per kv head
 constexpr float kTinyScale = 1e-37f;  // a logit scale that underflows must not make NaN of -inf
 
@@ -694,61 +694,82 @@ __device__ __forceinline__ float2 dec_row_stat(const float2* ml, int rows, int n
   return make_float2(ref, sum);
 }
 
-// Blocks [0, B * Hq * C/32): 32 columns of a query head's output, and its lse, from the
-// partials. The others (weights): acc_out[slot] = acc[slot] + sum over the group's heads of
-// the slot's softmax weight, from the logits of the split kernel and the joined statistics.
-// Its time is a chain of latencies (segment, statistics and values, sum), so the blocks are small, and the values
-// are loaded before the statistics that weigh them are known.
+// Blocks [0, B * Hq): output and lse of one query head from its partials. The others
+// (weights): acc_out[slot] = acc[slot] + sum over the group's heads of the slot's softmax
+// weight, from the logits of the split kernel and the joined statistics. Its time is a chain
+// of latencies (segment, statistics and values, sum): each warp takes every fourth partial,
+// a lane C/32 columns of it, and the values are loaded before the statistics that weigh them
+// are known.
 template <int C>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_per_tile,
                    int weight_blocks) {
-  __shared__ float red[kJoinThreads];
+  constexpr int kVec = C / 32;
+  __shared__ float red[kJoinThreads / 32][C];
   __shared__ float stat[kDecMaxGroup];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hq = p.Hq, per = p.cache.Hkv * p.HT;
-  const int n_join = p.cache.B * Hq * (C / 32);
+  const int n_join = p.cache.B * Hq;
   grid_dependency_wait();
 
   if ((int)blockIdx.x < n_join) {
-    const int bh = blockIdx.x / (C / 32), c = (blockIdx.x % (C / 32)) * 32 + lane;
-    const int b = bh / Hq, h = bh - b * Hq;
+    const int bh = blockIdx.x, b = bh / Hq, h = bh - b * Hq;
     const int kvh = h / p.G, g = h - kvh * p.G;
     const int item = b * per + kvh * p.HT + g / heads_per_tile;
     const int row = g % heads_per_tile;
-    const bool first = c == 0 && warp == 0;
     const int len = p.cache.length(b);
     const int2 seg = p.seg[item];      // not written for a sequence without keys
-    if (first && !p.cache.length_valid(b)) raise_device_error(kErrInvalid);
     if (len == 0) {                    // no key: o = 0, lse = -inf
-      if (warp == 0) p.O[(long long)bh * C + c] = __float2bfloat16(0.f);
-      if (first && p.lse != nullptr) p.lse[bh] = kNegInf;
+      if (tid < C) p.O[(long long)bh * C + tid] = __float2bfloat16(0.f);
+      if (tid == 0) {
+        if (p.lse != nullptr) p.lse[bh] = kNegInf;
+        if (!p.cache.length_valid(b)) raise_device_error(kErrInvalid);
+      }
       return;
     }
     if (seg.x == seg.y) return;        // one CTA had the whole item and finished it
     const int n = seg.y - seg.x + 1;
     const float2* ml = p.part_ml + ((long long)seg.x + item) * rows + row;
-    const float* po = p.part_o + (((long long)seg.x + item) * rows + row) * C + c;
-    constexpr int U = 8;
-    float v[U], m[U];
+    const float* po = p.part_o + (((long long)seg.x + item) * rows + row) * C + lane * kVec;
+    const long long step = (long long)rows * C;
+    struct alignas(kVec * 4) Vec { float x[kVec]; };
+    constexpr int U = 4;
+    Vec v[U];
+    float m[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long s = warp + 4 * u;
-      v[u] = s < n ? po[s * rows * C] : 0.f;
-      m[u] = s < n ? ml[s * rows].x : kNegInf;
+      const int s = warp + 4 * u;
+      m[u] = kNegInf;
+      if (s < n) {
+        v[u] = *reinterpret_cast<const Vec*>(po + s * step);
+        m[u] = ml[(long long)s * rows].x;
+      }
     }
     const float2 st = dec_row_stat(ml, rows, n, lane);       // every warp for itself
-    float y = 0.f;
+    float y[kVec];
 #pragma unroll
-    for (int u = 0; u < U; ++u) y += ex2(m[u] - st.x) * v[u];
-#pragma unroll 2
-    for (int s = warp + 4 * U; s < n; s += 4) y += ex2(ml[(long long)s * rows].x - st.x) * po[(long long)s * rows * C];
-    red[tid] = y;
+    for (int c = 0; c < kVec; ++c) y[c] = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (warp + 4 * u < n) {
+        const float f = ex2(m[u] - st.x);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) y[c] += f * v[u].x[c];
+      }
+#pragma unroll 4
+    for (int s = warp + 4 * U; s < n; s += 4) {
+      const Vec w = *reinterpret_cast<const Vec*>(po + s * step);
+      const float f = ex2(ml[(long long)s * rows].x - st.x);
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) y[c] += f * w.x[c];
+    }
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) red[warp][lane * kVec + c] = y[c];
     __syncthreads();
-    if (warp == 0) {
-      y = (red[lane] + red[32 + lane]) + (red[64 + lane] + red[96 + lane]);
-      p.O[(long long)bh * C + c] = __float2bfloat16(st.y == 0.f ? 0.f : y / st.y);
-      if (first && p.lse != nullptr)
+    if (tid < C) {
+      const float o = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
+      p.O[(long long)bh * C + tid] = __float2bfloat16(st.y == 0.f ? 0.f : o / st.y);
+      if (tid == 0 && p.lse != nullptr)
         p.lse[bh] = st.y == 0.f ? kNegInf : (st.x + log2f(st.y)) * kLn2;
     }
     return;

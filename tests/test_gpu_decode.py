@@ -559,10 +559,14 @@ def test_evict_special_weights():
         np.testing.assert_array_equal(f64(x), want[name])
 
 
-def test_evict_more_keys_than_shared_memory_holds():
-    """A row part larger than the keys' shared memory is read again on every pass: 20 rows of
-    45056 slots run one CTA each. Against a sort on the GPU."""
-    n, Hkv, page, C, budget = 45056, 80, 64, 64, 30000
+@pytest.mark.parametrize("n,Hkv,budget", [
+    (45056, 80, 30000),      # one CTA per row, its keys in the workspace
+    (131072, 2, 70001),      # a cluster per row, keys in shared memory
+    (400000, 1, 399999),     # a cluster per row, keys in the workspace; one slot goes
+])
+def test_evict_long_rows(n, Hkv, budget):
+    """Rows beyond what the oracle walks through: against a sort on the GPU."""
+    page, C = 64, 64
     P = n // page
     g = torch.Generator(device="cuda").manual_seed(0)
     k = torch.empty(P, Hkv, page, C, dtype=E4M3, device="cuda")
