@@ -652,8 +652,15 @@ def xattn_decode_attn(Q, cache: PagedCache, softmax_scale: float, O, workspace, 
           _ptr(lse), _ptr(acc_out), *_workspace(workspace))
 
 
+def _count(n, what: str) -> int:
+    n = int(n)
+    if not 0 <= n < 2 ** 31:         # ctypes would cut it to 32 bits
+        raise ValueError(f"{what} = {n} is not a count")
+    return n
+
+
 def xattn_cache_evict_workspace_size(cache: PagedCache, budget: int) -> int:
-    return int(_lib.xattn_cache_evict_workspace_size(cache._struct(), int(budget)))
+    return int(_lib.xattn_cache_evict_workspace_size(cache._struct(), _count(budget, "budget")))
 
 
 def xattn_cache_evict(cache: PagedCache, budget: int, workspace, recent: int = 0, sink: int = 0,
@@ -673,8 +680,8 @@ def xattn_cache_evict(cache: PagedCache, budget: int, workspace, recent: int = 0
         ord_out = cache.ordinal
     else:
         _want(ord_out, "ord_out", torch.int32, cache.ordinal.shape)
-    _call(_lib.xattn_cache_evict, dev, stream, cache._struct(), int(budget), int(recent), int(sink),
-          _per_sequence(seen, "seen", cache.B), acc_out.data_ptr(), ord_out.data_ptr(),
+    _call(_lib.xattn_cache_evict, dev, stream, cache._struct(), _count(budget, "budget"),
+          _count(recent, "recent"), _count(sink, "sink"), _per_sequence(seen, "seen", cache.B), acc_out.data_ptr(), ord_out.data_ptr(),
           *_workspace(workspace))
 
 

@@ -357,6 +357,8 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
     const int seg_tiles = min(at.tiles - at.tile, mine - n);
     const bool whole = seg_tiles == at.tiles;
     const int item = at.b * per + at.hk;
+    // logits of this lane's stores: head 2 (lane % 4) + (bit of lane/4), plus 8 per head tile
+    float* logits = p.logits + ((long long)at.b * p.Hq + h0 + i4 * 2 + (hr & 1)) * p.cache.capacity();
 
     // queries as the B operand: lane holds head lane/4 (of the 8 of head tile t)
     uint32_t qb[NT][kSteps][2];
@@ -482,13 +484,28 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
             mx[0] = fmax3(mx[0], sc[u][t][0], sc[u][t][2]);
             mx[1] = fmax3(mx[1], sc[u][t][1], sc[u][t][3]);
             if (p.logits != nullptr) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int h = i4 * 2 + (e & 1) + 8 * t, j = hr + 8 * (e >> 1);
-                if (h < heads && j < live[u])
-                  p.logits[((long long)at.b * p.Hq + h0 + h) * p.cache.capacity() + t_first + k0[u] + j] =
-                      sc[u][t][e] * mult[t][e & 1];
-              }
+              // The four lanes of keys r..r+3 (r = 0 or 4) transpose their 4 x 4 values: lane
+              // (half, d) gets the four keys r + 8 half .. of head 2i + d, one 16-byte store
+              // in place of four of 4 bytes.
+              const bool d1 = hr & 1, half1 = hr & 2;
+              const float v0 = sc[u][t][0] * mult[t][0], v1 = sc[u][t][1] * mult[t][1];
+              const float v2 = sc[u][t][2] * mult[t][0], v3 = sc[u][t][3] * mult[t][1];
+              const float a0 = d1 ? v1 : v0, a1 = d1 ? v3 : v2;
+              const float b0 = __shfl_xor_sync(0xffffffffu, d1 ? v0 : v1, 4);
+              const float b1 = __shfl_xor_sync(0xffffffffu, d1 ? v2 : v3, 4);
+              const float2 y0 = d1 ? make_float2(b0, a0) : make_float2(a0, b0);   // half 0
+              const float2 y1 = d1 ? make_float2(b1, a1) : make_float2(a1, b1);   // half 1
+              const float2 own = half1 ? y1 : y0;
+              const float2 out = half1 ? y0 : y1;
+              const float2 got = make_float2(__shfl_xor_sync(0xffffffffu, out.x, 8),
+                                             __shfl_xor_sync(0xffffffffu, out.y, 8));
+              const int h = i4 * 2 + d1 + 8 * t, j = (hr & 4) + (half1 ? 8 : 0);
+              // (slots of the quad behind the end lie inside the row, and are not read)
+              if (h < heads && j < live[u])
+                *reinterpret_cast<float4*>(logits + (long long)(8 * t) * p.cache.capacity() + t_first +
+                                           k0[u] + j) =
+                    half1 ? make_float4(got.x, got.y, own.x, own.y)
+                          : make_float4(own.x, own.y, got.x, got.y);
             }
           }
 #pragma unroll

@@ -882,3 +882,9 @@ def test_binding_refuses_on_the_gpu_too():
         xa.xattn_decode_attn(q, c, 0.1, o, ws.cpu())
     with pytest.raises(AttributeError):
         c.lens = c.lens.clone()
+    c = make_cache(2, [40, 50], 2, 64, 16)
+    for kw in (dict(budget=2 ** 32 + 5), dict(budget=-1), dict(budget=10, recent=2 ** 32), dict(budget=10, sink=-1)):
+        with pytest.raises(ValueError, match="count"):
+            xa.xattn_cache_evict(c, workspace=ws, **kw)
+    with pytest.raises(xa.XAttnError):
+        xa.xattn_cache_evict(c, 0, ws)
