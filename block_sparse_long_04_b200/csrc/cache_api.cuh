@@ -429,7 +429,6 @@ int xattn_cache_evict(const xattn_cache* cache, int budget, int recent, int sink
   p.budget = budget;
   p.recent = recent;
   p.sink = sink;
-  p.C = cache->C;
   p.row_bytes_log2 = ilog2(cache->C * (cache->kv_type == XATTN_KV_BF16 ? 2 : 1));
   p.keys = e.in_smem ? nullptr : reinterpret_cast<uint32_t*>(ws + e.off_keys);
   p.share = e.share;

@@ -31,6 +31,12 @@
 // largest element, less than the fp32 sums'. Sums, logits and statistics are fp32, o is
 // rounded once.
 //
+// Measured, whole calls, 32 query and 8 kv heads, C = 128: one sequence of 131072 bf16 slots
+// 85 us (0.54 GB, 6.3 TB/s), 32 ragged e4m3 sequences 94 us (0.59 GB, 6.2 TB/s), 8 of 32768
+// with weights 184 us (1.09 GB, 5.9 TB/s), one of 777 slots 6.8 us; 16 heads per kv head
+// 87 us for the first case. What binds is HBM; for e4m3 the widening (64 of 290
+// instructions per 16 keys and warp) comes close.
+//
 // Keys behind the end of a sequence inside its last page are masked, and their V rows
 // are zeroed in shared memory before use: 0 * NaN of a stale row would not be 0.
 // Every wait is bounded (sm100::mbar_wait).

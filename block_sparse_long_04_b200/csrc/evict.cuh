@@ -21,7 +21,8 @@
 // lists of the moves, needs one exchange of counts and then only ballots. The kernel is
 // bound by latencies (a row is a few KB to 1 MB, and each of its ~20 dependent steps is a
 // memory or barrier latency), not by bandwidth; its loops are kept short and rolled, since
-// code that runs once per CTA is fetched once per CTA too. Everything is counted in
+// code that runs once per CTA is fetched once per CTA too. 8 rows of 131072 slots (64 CTAs)
+// take 25 us of the call's 74, 128 rows of 4224 slots 12 of its 14. Everything is counted in
 // integers: the result does not depend on the order of the atomics.
 #pragma once
 #include "common.cuh"
@@ -48,7 +49,7 @@ struct EvictParams {
   int budget, recent, sink;
   uint32_t* keys;            // [rows, cluster, share * 5/4] where shared memory holds them not
   int share;                 // most slots of a CTA, a multiple of 4
-  int C, row_bytes_log2;
+  int row_bytes_log2;        // of a K or V row
 };
 
 // ascending key = descending weight; every NaN ranks above +inf, -0 equals +0
