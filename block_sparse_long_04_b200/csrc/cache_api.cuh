@@ -307,7 +307,7 @@ EvictPlan evict_plan(const xattn_cache* c, int budget) {
   while (e.cluster < 8 && e.rows * e.cluster * 2 <= 148 && cap / (e.cluster * 2) >= 2048) e.cluster *= 2;
   e.share = (int)((((cap + e.cluster - 1) / e.cluster) + 3) & ~3ll);
   e.in_smem = e.share <= kEvMaxKeys;
-  const size_t keys = (size_t)e.rows * e.cluster * (e.share + e.share / 4);
+  const size_t keys = (size_t)e.rows * e.cluster * evict_part_words(e.share);
   e.bytes = e.off_keys + (e.in_smem ? 0 : up(keys * sizeof(uint32_t)));
   return e;
 }

@@ -47,10 +47,17 @@ struct EvictParams {
   int32_t* mover;            // [rows, max_moves] pool rows they come from
   long long max_moves;
   int budget, recent, sink;
-  uint32_t* keys;            // [rows, cluster, share * 5/4] where shared memory holds them not
+  uint32_t* keys;            // [rows, cluster, evict_part_words] where shared memory holds them not
   int share;                 // most slots of a CTA, a multiple of 4
   int row_bytes_log2;        // of a K or V row
 };
+
+// Words of a CTA's part of the workspace: `share` (a multiple of 4) keys, a pool row for every
+// fourth slot, and up to the next multiple of four words, because the keys are stored and
+// loaded 16 bytes at a time and the parts lie one behind the other.
+__host__ __device__ constexpr long long evict_part_words(int share) {
+  return ((long long)share + share / 4 + 3) & ~3ll;
+}
 
 // ascending key = descending weight; every NaN ranks above +inf, -0 equals +0
 __device__ __forceinline__ uint32_t evict_key(float w, int ordinal, int safe_from, int sink) {
@@ -153,7 +160,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
   // the workspace: written and read by the warp alone
   uint32_t* part_keys = p.keys == nullptr
                             ? smem_keys
-                            : p.keys + ((long long)row * CL + rank) * (p.share + p.share / 4);
+                            : p.keys + ((long long)row * CL + rank) * evict_part_words(p.share);
   uint32_t* mykeys = part_keys + (lo - first);
   int* myrows = reinterpret_cast<int*>(part_keys + p.share) + (lo - first) / 4;
   {

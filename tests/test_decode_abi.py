@@ -207,6 +207,41 @@ def test_evict_workspace_size():
     assert size(cache(), 0) == 0 and size(None, 5) == 0
 
 
+def _evict_plan(B, Hkv, page, max_pages, budget):
+    """(rows, CTAs per row, most slots of one, bytes ahead of the keys) as the library plans them."""
+    def up(x):
+        return (x + 255) // 256 * 256
+
+    cap, rows, cluster = max_pages * page, B * Hkv, 1
+    while cluster < 8 and rows * cluster * 2 <= 148 and cap // (cluster * 2) >= 2048:
+        cluster *= 2
+    share = (-(-cap // cluster) + 3) // 4 * 4
+    moves = max(0, min(budget, cap - budget))
+    return rows, cluster, share, up(rows * 4) + 2 * up(rows * moves * 4)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_evict_keys_in_the_workspace_are_aligned(page):
+    """Rows too long for shared memory keep their keys (and pool rows, one per four slots) in the
+    workspace, one part per CTA. The parts are accessed 16 bytes at a time, so each takes a
+    multiple of 16 bytes, whatever the capacity, and the workspace holds them all."""
+    seen = set()
+    for B, Hkv in ((1, 1), (1, 8), (3, 1), (2, 8), (4, 8), (8, 8), (5, 7), (16, 8), (80, 1)):
+        for max_pages in [(41000 * n) // page + d for n in (1, 2, 4, 8, 10) for d in range(16)] + [8193, 5121]:
+            c = cache(B=B, Hkv=Hkv, C=64, page=page, max_pages=max_pages, num_pages=8)
+            rows, cluster, share, ahead = _evict_plan(B, Hkv, page, max_pages, 1000)
+            got = xa._lib.xattn_cache_evict_workspace_size(c, 1000)
+            if share <= 40960:                      # in shared memory
+                assert got == ahead
+                continue
+            part = (4 * (share + share // 4) + 15) // 16 * 16
+            assert got - ahead >= rows * cluster * part, (B, Hkv, max_pages)
+            assert got - ahead < rows * cluster * part + 256
+            if part != 5 * share:
+                seen.add(cluster)
+    # the shapes above do reach parts whose length alone is not a multiple of 16 bytes
+    assert seen >= {16: {2, 4, 8}, 32: {4, 8}, 64: {8}, 128: set()}[page]
+
 # ---------------------------------------------------- the binding's checks
 def test_binding_checks_tensors():
     bf = dict(dtype=torch.bfloat16)

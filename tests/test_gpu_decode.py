@@ -585,6 +585,61 @@ def test_evict_long_rows(n, Hkv, budget):
     assert torch.equal(w, flat.gather(1, got.long()))
 
 
+@pytest.mark.parametrize("B,Hkv,page,max_pages,in_workspace", [
+    (9, 8, 16, 2561, False),
+    (9, 8, 16, 5125, True),        # clusters of 2, 4, 4, 8, 8 CTAs
+    (4, 8, 32, 5121, True),
+    (4, 8, 16, 10241, True),
+    (1, 8, 64, 5121, True),
+    (3, 1, 16, 20501, True),
+])
+def test_evict_with_a_table_wider_than_the_rows(B, Hkv, page, max_pages, in_workspace):
+    """Tables made for long contexts, of odd lengths, over short sequences: the plan goes by the
+    table, so the selection's keys lie in the workspace, in one part per CTA of a cluster. The
+    same rows in a table just wide enough give the same cache."""
+    lens = [200 + 37 * b for b in range(B)]
+    c = make_cache(B, lens, Hkv, 64, page)
+    fill_eviction(c, page)
+    wide = clone_cache(c)
+    table = torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.max_pages] = c.page_table
+    wide = xa.PagedCache(wide.k_pages, wide.v_pages, table, wide.lens, acc=wide.acc, ordinal=wide.ordinal)
+    assert (xa.xattn_cache_evict_workspace_size(wide, 150) > 4 * max_pages * page * B * Hkv) == in_workspace
+    want = do.cache_evict(to_oracle(c), 150, 20, 4, (3 * c.lens).cpu().numpy())
+    run_evict(c, 150, 20, 4, 3 * c.lens)
+    run_evict(wide, 150, 20, 4, 3 * wide.lens)
+    assert same_cache(wide, c)
+    for name, t in (("k", wide.k_pages), ("v", wide.v_pages), ("acc", wide.acc), ("ordinal", wide.ordinal)):
+        np.testing.assert_array_equal(f64(t), want[name])
+
+
+@pytest.mark.parametrize("n,Hkv,page,max_pages,budget", [
+    (131000, 64, 16, 8193, 60000),     # a cluster of 2, both parts in use
+    (163000, 32, 32, 5121, 100001),    # of 4
+    (327700, 8, 64, 5121, 200002),     # of 8
+])
+def test_evict_long_rows_with_keys_in_the_workspace(n, Hkv, page, max_pages, budget):
+    """Long rows in tables whose parts of the workspace are not whole multiples of 16 bytes by
+    their length alone: against a sort on the GPU."""
+    C, P = 64, -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.zeros(P, Hkv, page, C, dtype=E4M3, device="cuda")
+    one = torch.ones(Hkv, device="cuda")
+    acc = torch.rand(P, Hkv, page, device="cuda", generator=g)
+    age = torch.arange(P * page, dtype=torch.int32, device="cuda").view(P, 1, page).expand(P, Hkv, page).contiguous()
+    table = torch.full((1, max_pages), -1, dtype=torch.int32, device="cuda")
+    table[0, :P] = torch.arange(P, dtype=torch.int32, device="cuda")
+    c = xa.PagedCache(k, k.clone(), table, torch.tensor([n], dtype=torch.int32, device="cuda"), one, one, acc, age)
+    flat = acc.permute(1, 0, 2).reshape(Hkv, -1)[:, :n]
+    safe = torch.arange(n, device="cuda") >= n - 500
+    order = torch.where(safe, float("inf"), flat).sort(dim=1, descending=True, stable=True).indices[:, :budget]
+    flat = flat.clone()
+    run_evict(c, budget, 500, 0)
+    got = c.ordinal.permute(1, 0, 2).reshape(Hkv, -1)[:, :budget]
+    assert torch.equal(got.sort(dim=1).values, order.int().sort(dim=1).values)
+    w = c.acc.permute(1, 0, 2).reshape(Hkv, -1)[:, :budget]
+    assert torch.equal(w, flat.gather(1, got.long()))
+
 # ------------------------------------------------- the operators as a user runs them
 def test_prefill_append_decode_evict_decode():
     """A prompt through the prefill, its keys into the cache, decoding steps that rotate,
