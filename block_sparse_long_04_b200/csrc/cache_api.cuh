@@ -373,7 +373,7 @@ int xattn_decode_attn(const xattn_heads* Q, const xattn_cache* cache, float soft
   if (!(softmax_scale > 0.f) || softmax_scale == __builtin_huge_valf()) return XATTN_EINVAL;
   if (empty) return XATTN_OK;
   if (!O || !aligned16(O) || !workspace || !aligned16(workspace)) return XATTN_EINVAL;
-  if (acc_out != nullptr && cache->acc == nullptr) return XATTN_EINVAL;
+  if (acc_out != nullptr && (cache->acc == nullptr || !aligned16(acc_out))) return XATTN_EINVAL;
   const DecodePlan d = decode_plan(cache, Q->heads, acc_out != nullptr);
   if (workspace_bytes < d.bytes) return XATTN_EINVAL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -403,7 +403,7 @@ typedef enum {
  *   acc                fp32 [num_pages, Hkv, page], accumulated attention weight of each
  *                      slot, or NULL
  *   ordinal            int32 [num_pages, Hkv, page], index of the slot's token in its
- *                      sequence, or NULL
+ *                      sequence, or NULL (acc and ordinal 16-byte aligned)
  *   page_table         int32 [B, max_pages];  lens  int32 [B], slots in use
  */
 typedef struct {
@@ -456,7 +456,8 @@ XATTN_API size_t xattn_decode_workspace_size(const xattn_cache* cache, int Hq, i
  *   lse      fp32 [B, Hq], natural-log log-sum-exp, or NULL
  *   acc_out  fp32 [num_pages, Hkv, page] or NULL: acc_out = acc + sum of p over the query
  *            heads of the slot's kv head, for the slots in use (the others are left as
- *            they were). May be cache->acc itself, and must not overlap it otherwise.
+ *            they were). May be cache->acc itself, and must not overlap it otherwise;
+ *            16-byte aligned.
  *   workspace  device buffer, 16-byte aligned; contents on entry are ignored
  * The sums and the softmax are fp32; results do not depend on the order in which the
  * GPU runs its blocks.
@@ -480,7 +481,8 @@ XATTN_API size_t xattn_cache_evict_workspace_size(const xattn_cache* cache, int 
  *   budget   >= 1;  recent, sink >= 0, recent + sink <= budget
  *   seen     int32 [B], as in xattn_cache_append, or NULL for lens
  *   acc_out, ord_out  like acc and ordinal; slots 0..n-1 are written. Each may be
- *            the cache's own array (in place), and must not overlap it otherwise.
+ *            the cache's own array (in place), and must not overlap it otherwise;
+ *            16-byte aligned.
  * cache->acc and cache->ordinal must be present.
  */
 XATTN_API int xattn_cache_evict(const xattn_cache* cache, int budget, int recent, int sink,

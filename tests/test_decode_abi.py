@@ -175,6 +175,12 @@ def test_decode_workspace_size():
     assert size(cache(B=0), 4, 0) == 0 and size(None, 4, 0) == 0 and size(cache(), 3, 0) == 0
 
 
+@pytest.mark.parametrize("off", [4, 8, 12])
+def test_decode_rejects_an_unaligned_acc_out(off):
+    """acc_out is stored 16 bytes at a time, like the cache's own acc."""
+    assert _decode(acc_out=FAKE + off) == EINVAL
+
+
 # ------------------------------------------------------------------ evict
 def _evict(c=None, budget=100, recent=8, sink=4, acc_out=FAKE, ord_out=FAKE, ws=FAKE, ws_bytes=1 << 40):
     return xa._lib.xattn_cache_evict(cache() if c is None else c, budget, recent, sink, None, acc_out,
