@@ -28,8 +28,14 @@
 // an error as large as the output's own rounding. e4m3 pages are widened to f16, which
 // holds them exactly. q is scaled there by a power of two per head so that its largest
 // element is in [1/2, 1]; below 2^-14 of that f16 loses bits, an error of 2^-25 of the
-// largest element, less than the fp32 sums'. Sums, logits and statistics are fp32, o is
-// rounded once.
+// largest element, less than the fp32 sums'. f16 weights end at 2^-25, too early for one
+// reference per head: beside a slot that takes nearly all the weight, and whose value may be 0,
+// the others would count in the sum and not in the output. So the reference follows the
+// tiles down too, and a weight is off by at most 2^-26 of the largest among the keys that
+// a warp takes together (32 neighbours at most), or by 2^-112 of the head's largest. (Tiles
+// with references of their own, scaled into the head's output, would hold 2^-38 of the largest
+// neighbour, and took 159 us instead of 136 for 32 sequences of 8192 slots with 16 heads per kv head.)
+// Sums, logits and statistics are fp32, o is rounded once.
 //
 // Measured, whole calls, 32 query and 8 kv heads, C = 128: one sequence of 131072 bf16 slots
 // 85 us (0.54 GB, 6.3 TB/s), 32 ragged e4m3 sequences 94 us (0.59 GB, 6.2 TB/s), 8 of 32768
@@ -52,6 +58,10 @@ constexpr int kDecThreads = 160;      // four MMA warps, one TMA warp
 constexpr int kDecMaxCtas = 444;      // 148 SMs x 3
 constexpr int kJoinThreads = 128;     // at least the largest C
 constexpr int kDecMaxGroup = 128;     // query heads per kv head
+// f16 weights of a tile (e4m3 pages): the largest lies between 2^kF16Low and 2^kF16High (65504
+// is the type's end), 2^kF16Set where the reference has just moved. Sums of weights and
+// outputs stay below 2^(kF16Span + 9 + 28): 448 at most, 2^28 keys of a warp.
+constexpr float kF16Low = 2.f, kF16Set = 12.f, kF16High = 15.f, kF16Span = 88.f;
 constexpr float kTinyScale = 1e-37f;  // a logit scale that underflows must not make NaN of -inf
 
 struct DecodeParams {
@@ -414,9 +424,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
 
     // reference, sum of this lane's keys, and O^T (columns lane/4, +8 of each 16), per head
     float m[NT][2], l[NT][2], o[NT][kSteps][4];
+    float peak[FP8 ? NT : 1][2];     // largest logit so far
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       m[t][0] = m[t][1] = kNegInf;
+      if (FP8) peak[t][0] = peak[t][1] = kNegInf;
       l[t][0] = l[t][1] = 0.f;
 #pragma unroll
       for (int c = 0; c < kSteps; ++c) o[t][c][0] = o[t][c][1] = o[t][c][2] = o[t][c][3] = 0.f;
@@ -520,20 +532,36 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
             for (int w = 4; w < 32; w <<= 1) mx[d] = fmaxf(mx[d], __shfl_xor_sync(0xffffffffu, mx[d], w));
             mx[d] *= mult[t][d];
           }
-          // the reference follows a head's maximum only when that has outgrown it by 2^8:
-          // the weights stay below 2^8 and a rescaling of O becomes rare
-          const bool grow[2] = {mx[0] > m[t][0] + 8.f, mx[1] > m[t][1] + 8.f};
-          if (__any_sync(0xffffffffu, grow[0] || grow[1])) {
+          // the reference moves only when a head's maximum has left a range around it, which
+          // bounds the weights and makes a rescaling of O rare. bf16 weights: up when it has
+          // been outgrown by 2^8. f16 weights: also down, so that those of this tile stay clear
+          // of that type's lower end, but never 2^kF16Span below the largest maximum so far.
+          bool move[2];
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            if (FP8) {
+              peak[t][d] = fmaxf(peak[t][d], mx[d]);
+              move[d] = fabsf(mx[d] - m[t][d] - 0.5f * (kF16Low + kF16High)) > 0.5f * (kF16High - kF16Low);
+            } else {
+              move[d] = mx[d] > m[t][d] + 8.f;
+            }
+          }
+          if (__any_sync(0xffffffffu, move[0] || move[1])) {
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-              const float f = grow[d] ? ex2(m[t][d] - mx[d]) : 1.f;
+              float to = mx[d];
+              if (FP8) {
+                move[d] = move[d] && mx[d] > kNegInf;
+                to = fmaxf(mx[d] - kF16Set, peak[t][d] - kF16Span);
+              }
+              const float f = move[d] ? ex2(m[t][d] - to) : 1.f;
               l[t][d] *= f;
 #pragma unroll
               for (int c = 0; c < kSteps; ++c) {
                 o[t][c][d] *= f;
                 o[t][c][2 + d] *= f;
               }
-              if (grow[d]) m[t][d] = mx[d];
+              if (move[d]) m[t][d] = to;
             }
           }
           const float ref[2] = {m[t][0] == kNegInf ? 0.f : m[t][0], m[t][1] == kNegInf ? 0.f : m[t][1]};

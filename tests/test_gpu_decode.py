@@ -384,6 +384,52 @@ def test_decode(lens, Hq, Hkv, C, page, weights, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,C,first", [(4, 1, 128, 5), (4, 2, 64, 1333), (16, 1, 128, 5)])
+@pytest.mark.parametrize("octaves", [20, 30, 60, 100])
+def test_decode_beside_a_slot_that_takes_nearly_all_the_weight(octaves, Hq, Hkv, C, first, e4m3):
+    """One slot whose value is 0 (an attention sink) outweighs each of the others by 2^octaves,
+    so the output is made of the small weights alone. The same pages serve 300 sequences, so
+    that a CTA walks many tiles, and from every start. Tolerance of the output as in
+    check_decode, and over e4m3 pages per slot 2^-26 of the largest weight among the 32
+    neighbouring slots that are weighed together (they are held in f16, that largest one at 4
+    or above, with an error of 2^-25) or 2^-112 of the head's largest; at most the weight itself."""
+    n, B, scale = 2500, 300, 1 / math.sqrt(C)
+    c = make_cache(21, [n], Hkv, C, 32, e4m3, eviction=False)
+    g = torch.Generator().manual_seed(4)
+    q = (torch.rand(1, 1, C, generator=g) + 0.5).bfloat16()     # one query: one key outweighs for every head
+    k, v = c.k_pages.float(), c.v_pages.float()
+    pg, r = do.cache_slot(to_oracle(c), 0, first)
+    k = k * 2.0 ** -5
+    k[pg, :, r] = octaves * math.log(2) / scale / q.float().sum().item()
+    if e4m3:
+        c.k_scale.mul_(2)            # the heavy key is below 448 scales
+        k[pg, :, r] /= c.k_scale[:, None]
+    v = v.abs() * 0.25 + (16.0 if e4m3 else 1.0)
+    v[pg, :, r] = 0
+    c.k_pages.copy_(k)
+    c.v_pages.copy_(v)
+    many = xa.PagedCache(c.k_pages, c.v_pages, c.page_table.expand(B, -1).contiguous(), c.lens.expand(B).contiguous(),
+                         c.k_scale, c.v_scale)
+    o, lse = run_decode(many, q.expand(B, Hq, C).contiguous().cuda(), scale)
+    oc, qd = to_oracle(c), f64(q)[0, 0]
+    wo, wl, _ = do.decode_attention(np.broadcast_to(qd, (1, Hq, C)), oc, scale)
+    for hq in range(Hq):
+        k, v = do.cache_rows(oc, "k", 0, hq * Hkv // Hq), do.cache_rows(oc, "v", 0, hq * Hkv // Hq)
+        x = scale * (k @ qd)
+        dx = (2 * C * U + (2.0 ** -24 if e4m3 else 0)) * scale * (np.abs(k) @ np.abs(qd)) + 8 * U * np.abs(x)
+        if e4m3:
+            dx = dx + 2.0 ** -25 * scale * np.abs(qd).max() * np.abs(k).sum(1)
+        p = np.exp(x - wl[0, hq])
+        assert p[first] > 0.9 and p.sum() - p[first] < 2.0 ** (14 - octaves)
+        tol = 2.0 ** -8 * np.abs(wo[0, hq]) + (p @ np.abs(v)) * (2 * dx.max() + 2.0 ** -20 + 2.0 ** -16) * 1.01
+        if e4m3:
+            top = np.maximum.reduceat(p, np.arange(0, n, 32)).repeat(32)[:n]
+            tol = tol + np.minimum(np.maximum(2.0 ** -26 * top, 2.0 ** -112 * p.max()), p) @ np.abs(v)
+        assert (np.abs(f64(o)[:, hq] - wo[0, hq]) <= tol).all(), hq
+        assert np.abs(wo[0, hq]).min() > 4 * tol.max()       # the outputs are not all tolerance
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("shift", [30.0, 300.0, -300.0])
 def test_decode_with_far_larger_and_smaller_logits(shift, e4m3):
     """Single keys whose logits tower over (or sink below) the others, early and late in
