@@ -23,8 +23,8 @@
 // O^T read from TMEM between the steps; the tensor pipe is not what binds here). P turns
 // from the accumulator's layout into the B operand's with movmatrix, in registers.
 //
-// Rounding. The weights enter P V as two 16-bit terms, p and what its rounding left (16 bits
-// together in bf16, 22 in f16), for one more MMA per tile; a single bf16 weight would add
+// Rounding. The weights enter P V as two 16-bit terms, p cut to its type and what that left (16
+// bits together in bf16, 22 in f16), for one more MMA per tile; a single bf16 weight would add
 // an error as large as the output's own rounding. e4m3 pages are widened to f16, which
 // holds them exactly. q is scaled there by a power of two per head so that its largest
 // element is in [1/2, 1]; below 2^-14 of that f16 loses bits, an error of 2^-25 of the
@@ -198,7 +198,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// rounded pair, and the pair of what the rounding left
+// Two 16-bit pairs whose sums are (x, y), x and y >= 0. f16: rounded, and what that left. bf16:
+// the next value below x, and what is left, which is never 0 or negative unless x is 0. Both
+// are multiplied with the same value, and an infinite one (e4m3 has none) must stay that
+// infinity: 0 * inf and inf - inf are NaN.
 template <bool F16>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint32_t* lo) {
   if (F16) {
@@ -206,8 +209,10 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint3
     *hi = *reinterpret_cast<const uint32_t*>(&h);
     *lo = pack_f16x2(x - __low2float(h), y - __high2float(h));
   } else {
-    *hi = pack_bf16x2(x, y);
-    *lo = pack_bf16x2(x - __uint_as_float(*hi << 16), y - __uint_as_float(*hi & 0xffff0000u));
+    const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+    const uint32_t hx = (ux - (ux != 0u)) & 0xffff0000u, hy = (uy - (uy != 0u)) & 0xffff0000u;
+    *hi = __byte_perm(hx, hy, 0x7632);
+    *lo = pack_bf16x2(x - __uint_as_float(hx), y - __uint_as_float(hy));
   }
 }
 // transposes an 8 x 8 matrix of 16-bit values (lane l: row l/4, columns 2(l%4), +1)

@@ -460,7 +460,11 @@ XATTN_API size_t xattn_decode_workspace_size(const xattn_cache* cache, int Hq, i
  *            16-byte aligned.
  *   workspace  device buffer, 16-byte aligned; contents on entry are ignored
  * The sums and the softmax are fp32; results do not depend on the order in which the
- * GPU runs its blocks.
+ * GPU runs its blocks. What slots in use hold takes part: NaN in K, or in V, makes NaN of
+ * the outputs it reaches. Infinities of one sign in a column of V make that infinity, where
+ * their weights are above 2^-100 of the head's largest; times a weight of 0 (a logit of
+ * -inf), and of both signs, they make NaN. Sums of weight * value are formed before they
+ * are divided by the sum of the weights: finite values beyond 2^90 may overflow.
  */
 XATTN_API int xattn_decode_attn(const xattn_heads* Q, const xattn_cache* cache,
                                 float softmax_scale, void* O, float* lse, float* acc_out,

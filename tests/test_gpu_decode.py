@@ -491,6 +491,33 @@ def test_decode_infinities_and_nan_in_reach():
     assert (o == 0).all() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("lens,slot", [([1, 30], 0), ([50, 9], 19), ([20000, 5], 7777)])
+@pytest.mark.parametrize("C,Hq,Hkv", [(64, 4, 2), (128, 16, 1)])
+def test_decode_infinite_values_in_reach(lens, slot, C, Hq, Hkv):
+    """Infinite values in use make their columns that infinity, or NaN where both signs meet;
+    every other column is as if they were not there."""
+    c = make_cache(31, lens, Hkv, C, 16)
+    q = (0.5 * torch.randn(2, Hq, C, generator=torch.Generator().manual_seed(6))).bfloat16().cuda()
+    t = c.page_table.cpu()
+    inf, at = float("inf"), (int(t[0, slot // 16]), Hkv - 1, slot % 16)
+    fine = clone_cache(c)
+    o, lse = run_decode(fine, q, 1 / math.sqrt(C))
+    want = o.clone()
+    mine = slice((Hkv - 1) * Hq // Hkv, Hq)            # the query heads of that kv head
+    c.v_pages[at[0], at[1], at[2], 3] = inf
+    c.v_pages[at[0], at[1], at[2], C - 1] = -inf
+    want[0, mine, 3], want[0, mine, C - 1] = inf, -inf
+    if lens[0] > 1:                                    # infinities of both signs: NaN
+        other = (slot + 5) % lens[0]
+        for s, x in ((slot, inf), (other, -inf)):
+            c.v_pages[int(t[0, s // 16]), Hkv - 1, s % 16, 9] = x
+        want[0, mine, 9] = float("nan")
+    got, lse2 = run_decode(c, q, 1 / math.sqrt(C))
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    ok = ~torch.isnan(want)
+    assert torch.equal(got[ok], want[ok]) and torch.equal(lse, lse2)
+
+
 def test_decode_strided_queries_and_4d():
     C, lens = 128, [70, 9]
     c = make_cache(12, lens, 2, C, 16, eviction=False)
