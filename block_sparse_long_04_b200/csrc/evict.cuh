@@ -184,7 +184,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
       for (int u = 0; u < U; ++u) {
         const int s = s0 + u * 128;
         if (s >= hi) break;
-        uint4 k = make_uint4(~0u, ~0u, ~0u, ~0u);     // a bad page's: never wanted before another
+        uint4 k;
         if (at[u] >= 0) {
           k = make_uint4(evict_key(w[u].x, o[u].x, safe_from, p.sink),
                          evict_key(w[u].y, o[u].y, safe_from, p.sink),
@@ -202,10 +202,14 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
             }
           }
         } else {
+          // A bad page's slots have no rows to give or to take. Below n they stay (as safe ones:
+          // n slots cannot come before them), from n on they go (the slots below n, bad ones
+          // among them, are enough). So neither list of the moves names one.
           raise_device_error(kErrInvalid);
+          k = make_uint4(s < n ? 0u : ~0u, s + 1 < n ? 0u : ~0u, s + 2 < n ? 0u : ~0u, s + 3 < n ? 0u : ~0u);
         }
         *reinterpret_cast<uint4*>(mykeys + (s - lo)) = k;     // (from hi on: written, never read)
-        myrows[(s - lo) / 4] = at[u] >= 0 ? at[u] : -8;       // a bad page's stay below 0
+        myrows[(s - lo) / 4] = at[u];
       }
     }
     __syncwarp();
@@ -360,7 +364,6 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
   const int32_t* mover = p.mover + row * p.max_moves;
   for (int m = (blockIdx.x * kEvMoveThreads + threadIdx.x) >> lanes_log2; m < count; m += step) {
     const long long to = hole[m], from = mover[m];
-    if (to < 0 || from < 0) continue;        // a bad page: the selection raised the error
     const uint4 k = *reinterpret_cast<const uint4*>(kp + (from << p.row_bytes_log2));
     const uint4 v = *reinterpret_cast<const uint4*>(vp + (from << p.row_bytes_log2));
     *reinterpret_cast<uint4*>(kp + (to << p.row_bytes_log2)) = k;

@@ -481,7 +481,8 @@ XATTN_API size_t xattn_cache_evict_workspace_size(const xattn_cache* cache, int 
  * below n (ascending) takes the row, acc and ordinal of the i-th kept slot from the end.
  * The order of slots carries no meaning for xattn_decode_attn; ordinals tell the tokens.
  * lens is not changed, because layers may share it: clamp it to budget after the last
- * layer. Slots from n on are left as they were.
+ * layer. Slots from n on are left as they were. Slots of a bad page (see above) have no
+ * rows: those below n keep their places, and the others are chosen for the rest.
  *   budget   >= 1;  recent, sink >= 0, recent + sink <= budget
  *   seen     int32 [B], as in xattn_cache_append, or NULL for lens
  *   acc_out, ord_out  like acc and ordinal; slots 0..n-1 are written. Each may be

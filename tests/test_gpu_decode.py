@@ -952,6 +952,52 @@ def test_bad_pages_touch_nothing_and_raise(bad):
     assert _error() == xa.XATTN_EINVAL
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens,Hkv,page,budget,bad", [
+    ([100, 57], 2, 16, 50, [1]),               # below the budget
+    ([100, 57], 2, 16, 50, [4]),               # above it
+    ([100, 57], 2, 16, 50, [3]),               # across it
+    ([100, 57], 1, 16, 50, [0, 1, 2, 3, 4]),
+    ([100, 57], 1, 16, 50, [0, 1, 2, 3, 4, 5, 6]),   # every page
+    ([9000, 100], 1, 64, 4000, [0, 7, 62, 63, 100, 140]),      # a cluster of CTAs
+])
+def test_evict_leaves_bad_pages_out(lens, Hkv, page, budget, bad, e4m3):
+    """Slots of bad pages keep their places below the budget; of the others as many stay as have
+    a place there, and none of them is lost. Nothing else is written."""
+    c = make_cache(51, lens, Hkv, 64, page, e4m3)
+    fill_eviction(c, 3, ties=True)
+    good = c.page_table.clone()
+    c.page_table[0, bad] = torch.tensor([-1, c.num_pages, 2 ** 31 - 1], dtype=torch.int32).cuda()[
+        torch.arange(len(bad)) % 3]
+    before, seen = to_oracle(c), (3 * c.lens).cpu().numpy()
+    want = do.cache_evict(dict(before, lens=np.array([0, lens[1]]), table=good.cpu().numpy()), budget, 8, 4, seen)
+    where = {s: do.cache_slot(before, 0, s) for s in range(lens[0]) if s // page not in bad}
+    n = min(budget, lens[0])
+    room = sum(s < n for s in where)
+    for h in range(Hkv):
+        slots = sorted(where)
+        kept = do.evict_kept([before["acc"][where[s][0], h, where[s][1]] for s in slots],
+                             [before["ordinal"][where[s][0], h, where[s][1]] for s in slots], room, seen[0], 8, 4)
+        kept = {slots[i] for i in kept}
+        holes = [s for s in slots if s < n and s not in kept]
+        movers = sorted((s for s in kept if s >= n), reverse=True)
+        assert len(holes) == len(movers)
+        for to, frm in zip(holes, movers):
+            for name in ("k", "v", "acc", "ordinal"):
+                want[name][where[to][0], h, where[to][1]] = before[name][where[frm][0], h, where[frm][1]]
+    assert _error() == xa.XATTN_OK
+    acc_out, ord_out = c.acc.clone(), c.ordinal.clone()
+    apart = clone_cache(c)
+    run_evict(apart, budget, 8, 4, 3 * c.lens, acc_out=acc_out, ord_out=ord_out)
+    assert _error() == xa.XATTN_EINVAL
+    run_evict(c, budget, 8, 4, 3 * c.lens)
+    assert _error() == xa.XATTN_EINVAL
+    for name, x, y in (("k", c.k_pages, apart.k_pages), ("v", c.v_pages, apart.v_pages), ("acc", c.acc, acc_out),
+                       ("ordinal", c.ordinal, ord_out)):
+        np.testing.assert_array_equal(f64(x), want[name])
+        assert torch.equal(raw(x), raw(y))
+
+
 def test_bad_lengths_and_counts_touch_nothing_and_raise():
     C = 64
     c = make_cache(2, [40, 50], 2, C, 16)
