@@ -288,6 +288,30 @@ def test_append_e4m3_special_values():
         assert torch.equal(raw(pages[0, :, 0])[~nan], raw(want)[~nan])
 
 
+def test_append_e4m3_quotients_of_every_value():
+    """Every finite bf16 value over scales of many sizes, those among them whose quotients lie
+    next to the middle of two e4m3 values, bit for bit against torch's division and conversion."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = x[torch.isfinite(x.float())].view(-1, 64)
+    mids = [1 + (2 * i + 1) / 16 for i in range(8)]
+    f32 = torch.float32
+    scales = torch.cat([torch.rand(16, generator=torch.Generator().manual_seed(0)) * 0.05 + 1e-3,
+                        torch.tensor([1.0, 0.5, 3.0, 1 / 3, 448.0, 1 / 448, 2.0 ** -126, 2.0 ** -130, 2.0 ** 127,
+                                      3.0e38, 1e-30, 1e30], dtype=f32),
+                        torch.tensor([a / m for m in mids for a in (1.0, 1.0078125, 1.9921875)], dtype=f32)])
+    for s in torch.stack([scales, scales.flip(0)], 1):
+        c = xa.PagedCache.allocate(1, 2, 64, x.shape[0] // 64 + 1, x.shape[0] // 64 + 1, page=64, dtype=E4M3,
+                                   k_scale=s.cuda(), v_scale=s.flip(0).contiguous().cuda())
+        c.lens.fill_(x.shape[0])
+        rows = x.cuda()[None, None].expand(1, 2, -1, -1)
+        xa.xattn_cache_append(rows, rows, c)
+        for pages, sc in ((c.k_pages, s), (c.v_pages, s.flip(0))):
+            for h in range(2):
+                want = (x.float() / sc[h]).clamp(-448, 448).to(E4M3)
+                got = pages[:, h].reshape(-1, 64)[:x.shape[0]].cpu()
+                assert torch.equal(raw(got), raw(want)), sc[h]
+
+
 # ------------------------------------------------------------------ decode
 def run_decode(c, q, scale, weights=False, acc_out=None, stream=None):
     B, Hq, C = q.shape
@@ -845,6 +869,40 @@ def test_on_a_side_stream_and_in_graphs():
         assert same_cache(s[0], new[0])
 
 
+def test_captured_step_after_a_fork():
+    """In a capture, calls behind a join of two streams and behind a copy, whose predecessors are
+    not just one kernel."""
+    c = make_cache(54, [40, 21], 2, 64, 16)
+    q = torch.randn(2, 8, 1, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    kv = torch.randn(2, 2, 2, 1, 64, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    src = [c.lens.clone(), c.page_table.clone()]
+    rot, pos = xa.Rotary.make((32,)), (c.lens - 1).view(2, 1, 1).clone()
+    qo, o = torch.empty_like(q), torch.empty_like(q)
+    ws = torch.empty(xa.xattn_decode_workspace_size(c, 8, True), dtype=torch.uint8, device="cuda")
+    ref = clone_cache(c)
+    xa.xattn_rope_append(q, kv[0], kv[1], pos, rot, ref, qo)
+    xa.xattn_decode_attn(qo, ref, 0.125, o, ws, weights=True)
+    want = o.clone()
+    c.lens.zero_()
+    c.page_table.fill_(-1)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            c.lens.copy_(src[0])
+        c.page_table.copy_(src[1])
+        main.wait_stream(side)
+        xa.xattn_rope_append(q, kv[0], kv[1], pos, rot, c, qo)
+        xa.xattn_decode_attn(qo, c, 0.125, o, ws, weights=True)
+        c.lens.add_(0)
+    o.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and same_cache(c, ref)
+
+
 def test_steps_without_a_pause_equal_steps_with_one():
     """Lengths, pages and queries change between calls that nothing waits for; the same steps
     with a synchronisation after every call give the same bits. (The calls overlap their
@@ -950,6 +1008,26 @@ def test_bad_pages_touch_nothing_and_raise(bad):
     ws = poisoned(xa.xattn_cache_evict_workspace_size(c, 20), torch.uint8)
     xa.xattn_cache_evict(c, 20, ws, recent=2)
     assert _error() == xa.XATTN_EINVAL
+
+
+def test_append_beside_a_bad_page_writes_its_own_slots_only():
+    """Every pool row after an append that reaches a bad page."""
+    c = make_cache(53, [40, 50], 2, 64, 16)
+    fill_eviction(c, 1)
+    c.page_table[0, 1] = -1                       # slots 16..31 of sequence 0
+    before = clone_cache(c)
+    kv = torch.randn(2, 2, 2, 20, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    xa.xattn_cache_append(kv[0], kv[1], c)        # slots 20..39 and 30..49
+    assert _error() == xa.XATTN_EINVAL
+    want = clone_cache(before)
+    for b, n in ((0, 40), (1, 50)):
+        for s in range(n - 20, n):
+            pg, r = int(before.page_table[b, s // 16]), s % 16
+            if pg < 0:
+                continue
+            want.k_pages[pg, :, r], want.v_pages[pg, :, r] = kv[0][b, :, s - n + 20], kv[1][b, :, s - n + 20]
+            want.acc[pg, :, r], want.ordinal[pg, :, r] = 0, s
+    assert same_cache(c, want)
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
