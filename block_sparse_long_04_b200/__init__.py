@@ -87,6 +87,7 @@ SIGNATURES.update({
     "xattn_rope_append": (_I, [_S, _S, _S, _S, _S, _I, _P, _P, _S, _P]),
     "xattn_decode_workspace_size": (_Z, [_S, _I, _I]),
     "xattn_decode_attn": (_I, [_S, _S, _F, _P, _P, _P, _P, _Z, _P]),
+    "xattn_decode_attn_ex": (_I, [_S, _S, _P, _F, _P, _P, _P, _P, _Z, _P]),
     "xattn_cache_evict_workspace_size": (_Z, [_S, _I]),
     "xattn_cache_evict": (_I, [_S, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
 })
@@ -617,13 +618,14 @@ def xattn_decode_workspace_size(cache: PagedCache, Hq: int, weights: bool = Fals
 
 
 def xattn_decode_attn(Q, cache: PagedCache, softmax_scale: float, O, workspace, lse=None,
-                      weights: bool = False, acc_out=None, stream=None) -> None:
+                      weights: bool = False, acc_out=None, stream=None, n_new=None) -> None:
     """O <- attention of one query per sequence and head over the cache's slots in use.
 
     Q and O [B, Hq, C] or [B, Hq, 1, C]; Q at any strides, O contiguous; lse fp32 [B, Hq].
     weights adds every slot's softmax weight, summed over the query heads of its KV head,
-    to cache.acc, into acc_out (default: cache.acc itself)."""
-    dev = _device_of(Q, cache.k_pages, O, workspace, lse, acc_out)
+    to cache.acc, into acc_out (default: cache.acc itself). n_new[b] is 0 for an idle
+    sequence, whose O is 0 and whose weights stay, and 1 for the others (default)."""
+    dev = _device_of(Q, cache.k_pages, O, workspace, lse, acc_out, n_new)
     shape = Q.shape
     if len(shape) == 3:
         B, H, C = shape
@@ -648,8 +650,8 @@ def xattn_decode_attn(Q, cache: PagedCache, softmax_scale: float, O, workspace, 
             _want(acc_out, "acc_out", torch.float32, cache.acc.shape)
     elif acc_out is not None:
         raise ValueError("acc_out needs weights=True")
-    _call(_lib.xattn_decode_attn, dev, stream, q, cache._struct(), float(softmax_scale), O.data_ptr(),
-          _ptr(lse), _ptr(acc_out), *_workspace(workspace))
+    _call(_lib.xattn_decode_attn_ex, dev, stream, q, cache._struct(), _per_sequence(n_new, "n_new", cache.B),
+          float(softmax_scale), O.data_ptr(), _ptr(lse), _ptr(acc_out), *_workspace(workspace))
 
 
 def _count(n, what: str) -> int:
@@ -706,11 +708,14 @@ class DecodeBuffers:
 
 def xattn_decode_step(Q, K, V, pos, rotary: Rotary, cache: PagedCache, bufs: DecodeBuffers, seen=None,
                       weights: bool = False, softmax_scale: Optional[float] = None,
-                      stream=None) -> torch.Tensor:
+                      stream=None, n_new=None) -> torch.Tensor:
     """One token per sequence through a layer after its prefill: rotate Q and K by pos, append
     K and V to the cache (cache.lens already counts the token), attend; returns bufs.O.
-    weights accumulates the slots' softmax weights in cache.acc, for xattn_cache_evict."""
+    weights accumulates the slots' softmax weights in cache.acc, for xattn_cache_evict. A
+    batch with empty, finished or waiting sequences gives n_new: 0 for those (their rows are
+    not read, their cache is left as it is, their O is 0), 1 for the others."""
     scale = 1.0 / math.sqrt(cache.C) if softmax_scale is None else softmax_scale
-    xattn_rope_append(Q, K, V, pos, rotary, cache, bufs.Q, seen=seen, stream=stream)
-    xattn_decode_attn(bufs.Q, cache, scale, bufs.O, bufs.workspace, bufs.lse, weights, stream=stream)
+    xattn_rope_append(Q, K, V, pos, rotary, cache, bufs.Q, n_new, seen, stream)
+    xattn_decode_attn(bufs.Q, cache, scale, bufs.O, bufs.workspace, bufs.lse, weights, n_new=n_new,
+                      stream=stream)
     return bufs.O

@@ -76,6 +76,7 @@ CacheView view_of(const xattn_cache* c) {
   v.ordinal = c->ordinal;
   v.page_table = c->page_table;
   v.lens = c->lens;
+  v.n_new = nullptr;
   v.B = c->B;
   v.Hkv = c->Hkv;
   v.page_log2 = ilog2(c->page);
@@ -365,6 +366,13 @@ size_t xattn_decode_workspace_size(const xattn_cache* cache, int Hq, int weights
 int xattn_decode_attn(const xattn_heads* Q, const xattn_cache* cache, float softmax_scale, void* O,
                       float* lse, float* acc_out, void* workspace, size_t workspace_bytes,
                       void* stream) {
+  return xattn_decode_attn_ex(Q, cache, nullptr, softmax_scale, O, lse, acc_out, workspace,
+                              workspace_bytes, stream);
+}
+
+int xattn_decode_attn_ex(const xattn_heads* Q, const xattn_cache* cache, const int32_t* n_new,
+                         float softmax_scale, void* O, float* lse, float* acc_out, void* workspace,
+                         size_t workspace_bytes, void* stream) {
   if (Q == nullptr) return XATTN_EINVAL;
   bool empty;
   int rc = check_decode(cache, Q->heads, &empty);
@@ -379,6 +387,7 @@ int xattn_decode_attn(const xattn_heads* Q, const xattn_cache* cache, float soft
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeParams p = {};
   p.cache = view_of(cache);
+  p.cache.n_new = n_new;
   p.q = static_cast<const bf16*>(Q->data);
   p.q_sb = Q->stride_b;
   p.q_sh = Q->stride_h;

@@ -346,7 +346,7 @@ const char* xattn_status_string(int status) {
   return "unknown status";
 }
 
-int xattn_version(void) { return 201; }
+int xattn_version(void) { return 202; }
 
 size_t xattn_score_workspace_size(int B, int Hq, int M, int stride, int block, int causal) {
   if (B < 0 || Hq < 0 || M < 0 || block != 128 || !stride_supported(stride) || M % block)

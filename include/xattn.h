@@ -73,7 +73,8 @@ typedef enum {
 XATTN_API const char* xattn_status_string(int status);
 
 /* Library ABI version (major*100 + minor); 200 since the workspace-size
- * functions take the causal flag, 201 with the decoding operators. */
+ * functions take the causal flag, 201 with the decoding operators, 202 with
+ * xattn_decode_attn_ex. */
 XATTN_API int xattn_version(void);
 
 /*
@@ -469,6 +470,18 @@ XATTN_API size_t xattn_decode_workspace_size(const xattn_cache* cache, int Hq, i
 XATTN_API int xattn_decode_attn(const xattn_heads* Q, const xattn_cache* cache,
                                 float softmax_scale, void* O, float* lse, float* acc_out,
                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * xattn_decode_attn_ex - xattn_decode_attn for a batch in which some sequences are idle.
+ *   n_new   int32 [B], the step's new tokens of each sequence as in xattn_rope_append (with
+ *           T = 1), or NULL for one everywhere. A sequence with 0 gets O = 0, lse = -inf, its
+ *           query is not read and its slots of acc_out are left as they were. Other values
+ *           than 0 and 1 count as 0 and raise XATTN_EINVAL in the device error word.
+ */
+XATTN_API int xattn_decode_attn_ex(const xattn_heads* Q, const xattn_cache* cache,
+                                   const int32_t* n_new, float softmax_scale, void* O, float* lse,
+                                   float* acc_out, void* workspace, size_t workspace_bytes,
+                                   void* stream);
 
 /* Workspace bytes of xattn_cache_evict; 0 for bad arguments. */
 XATTN_API size_t xattn_cache_evict_workspace_size(const xattn_cache* cache, int budget);

@@ -175,6 +175,19 @@ def test_decode_workspace_size():
     assert size(cache(B=0), 4, 0) == 0 and size(None, 4, 0) == 0 and size(cache(), 3, 0) == 0
 
 
+@pytest.mark.parametrize("kw,want", [
+    (dict(), EINVAL),                                            # a workspace of no bytes
+    (dict(Q=heads(3)), EINVAL), (dict(Q=heads(258)), EUNSUP), (dict(c=cache(page=48)), EUNSUP),
+    (dict(acc_out=FAKE + 4), EINVAL), (dict(c=cache(acc=None), acc_out=FAKE), EINVAL), (dict(scale=-1.0), EINVAL),
+    (dict(c=cache(B=0)), OK), (dict(Q=heads(0)), OK),
+])
+def test_decode_with_idle_sequences_rejects_on_host(kw, want):
+    a = dict(c=cache(), Q=heads(4), scale=0.1, acc_out=None)
+    a.update(kw)
+    for n_new in (None, FAKE):
+        assert xa._lib.xattn_decode_attn_ex(a["Q"], a["c"], n_new, a["scale"], FAKE, None, a["acc_out"], FAKE, 0,
+                                            None) == want
+
 @pytest.mark.parametrize("off", [4, 8, 12])
 def test_decode_rejects_an_unaligned_acc_out(off):
     """acc_out is stored 16 bytes at a time, like the cache's own acc."""

@@ -813,6 +813,43 @@ def test_decode_step_is_its_two_calls(e4m3):
     check_decode(b, qo[:, :, 0], 0.125, o2, lse2, before, f64(b.acc))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_step_with_idle_sequences(e4m3):
+    """A batch in which one sequence is empty, one has finished and one waits: the others' step
+    is that of a batch without them, and theirs writes nothing but zero outputs."""
+    Hq, Hkv, C, lens = 8, 2, 64, [40, 0, 33, 1, 200]
+    c = make_cache(61, lens, Hkv, C, 16, e4m3)
+    go = torch.tensor([1, 0, 0, 1, 0], dtype=torch.int32, device="cuda")
+    on = [0, 3]
+    x = torch.randn(5, 1, Hq + 2 * Hkv, C, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    x[~go.bool()] = float("nan")                       # an idle row holds anything
+    q, k, v = (t.transpose(1, 2) for t in x.split([Hq, Hkv, Hkv], 2))
+    rot, seen = xa.Rotary.make((32,)), c.lens + 7
+    pos = (seen - 1).view(5, 1, 1)
+    want = clone_cache(c)
+    few = xa.PagedCache(want.k_pages, want.v_pages, want.page_table[on].contiguous(), want.lens[on].contiguous(),
+                        want.k_scale, want.v_scale, want.acc, want.ordinal)
+    fbufs = xa.DecodeBuffers.allocate(few, Hq, weights=True, with_lse=True)
+    xa.xattn_decode_step(q[on], k[on], v[on], pos[on].contiguous(), rot, few, fbufs, seen=seen[on].contiguous(),
+                         weights=True)
+    bufs = xa.DecodeBuffers.allocate(c, Hq, weights=True, with_lse=True)
+    for t in (bufs.Q, bufs.O, bufs.lse, bufs.workspace):
+        t.view(torch.uint8).fill_(0xFF)
+    o = xa.xattn_decode_step(q, k, v, pos, rot, c, bufs, seen=seen, weights=True, n_new=go)
+    assert same_cache(c, want)
+    assert torch.equal(o[~go.bool()], torch.zeros_like(o[~go.bool()]))
+    assert torch.isneginf(bufs.lse[~go.bool()]).all()
+    # (an idle sequence has no tiles, so the work is split as without it: the same bits)
+    assert torch.equal(o[on], fbufs.O) and torch.equal(bufs.lse[on], fbufs.lse)
+    assert _error() == xa.XATTN_OK
+    # nobody has a token; then counts that are none
+    before = clone_cache(c)
+    for n, want_error in ((0, xa.XATTN_OK), (2, xa.XATTN_EINVAL), (-1, xa.XATTN_EINVAL), (2 ** 31 - 1, xa.XATTN_EINVAL)):
+        o = xa.xattn_decode_step(q, k, v, pos, rot, c, bufs, seen=seen, weights=True, n_new=torch.full_like(go, n))
+        assert _error() == want_error
+        assert (o == 0).all() and torch.isneginf(bufs.lse).all() and same_cache(c, before)
+
+
 def test_on_a_side_stream_and_in_graphs():
     """A decoding step captured into a graph and replayed with new inputs, lengths and pages,
     next to another graph with a workspace of its own."""
