@@ -378,7 +378,8 @@ int xattn_decode_attn_ex(const xattn_heads* Q, const xattn_cache* cache, const i
   int rc = check_decode(cache, Q->heads, &empty);
   if (rc != XATTN_OK) return rc;
   if ((rc = check_heads(Q, cache->B, 1, false)) != XATTN_OK) return rc;
-  if (!(softmax_scale > 0.f) || softmax_scale == __builtin_huge_valf()) return XATTN_EINVAL;
+  // (in log2 units, as the kernels take it, the scale must be finite too)
+  if (!(softmax_scale > 0.f) || softmax_scale * kLog2e == __builtin_huge_valf()) return XATTN_EINVAL;
   if (empty) return XATTN_OK;
   if (!O || !aligned16(O) || !workspace || !aligned16(workspace)) return XATTN_EINVAL;
   if (acc_out != nullptr && (cache->acc == nullptr || !aligned16(acc_out))) return XATTN_EINVAL;

@@ -194,6 +194,11 @@ def test_decode_rejects_an_unaligned_acc_out(off):
     assert _decode(acc_out=FAKE + off) == EINVAL
 
 
+@pytest.mark.parametrize("scale", [2.5e38, 3.4e38])
+def test_decode_rejects_a_scale_that_overflows_in_log2_units(scale):
+    assert _decode(scale=scale) == EINVAL
+
+
 # ------------------------------------------------------------------ evict
 def _evict(c=None, budget=100, recent=8, sink=4, acc_out=FAKE, ord_out=FAKE, ws=FAKE, ws_bytes=1 << 40):
     return xa._lib.xattn_cache_evict(cache() if c is None else c, budget, recent, sink, None, acc_out,
