@@ -650,8 +650,9 @@ def xattn_decode_attn(Q, cache: PagedCache, softmax_scale: float, O, workspace, 
             _want(acc_out, "acc_out", torch.float32, cache.acc.shape)
     elif acc_out is not None:
         raise ValueError("acc_out needs weights=True")
-    _call(_lib.xattn_decode_attn_ex, dev, stream, q, cache._struct(), _per_sequence(n_new, "n_new", cache.B),
-          float(softmax_scale), O.data_ptr(), _ptr(lse), _ptr(acc_out), *_workspace(workspace))
+    new = None if n_new is None else _per_sequence(n_new, "n_new", cache.B)
+    _call(_lib.xattn_decode_attn_ex, dev, stream, q, cache._struct(), new, float(softmax_scale), O.data_ptr(),
+          _ptr(lse), _ptr(acc_out), *_workspace(workspace))
 
 
 def _count(n, what: str) -> int:

@@ -76,7 +76,6 @@ CacheView view_of(const xattn_cache* c) {
   v.ordinal = c->ordinal;
   v.page_table = c->page_table;
   v.lens = c->lens;
-  v.n_new = nullptr;
   v.B = c->B;
   v.Hkv = c->Hkv;
   v.page_log2 = ilog2(c->page);
@@ -248,9 +247,10 @@ template <int C, bool FP8, int NT>
 int launch_decode_split(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p,
                         cudaStream_t st) {
   using L = Decode<C, FP8, NT>;
-  auto kern = decode_split_kernel<C, FP8, NT>;
-  static unsigned long long done = 0;
-  if (ensure_smem_limit(kern, L::kSmem, &done) != XATTN_OK) return XATTN_ECUDA;
+  static unsigned long long done[2] = {0, 0};
+  const bool idle = p.n_new != nullptr;
+  auto kern = idle ? decode_split_kernel<C, FP8, NT, true> : decode_split_kernel<C, FP8, NT, false>;
+  if (ensure_smem_limit(kern, L::kSmem, &done[idle]) != XATTN_OK) return XATTN_ECUDA;
   return launch(kern, dim3(148 * L::kPerSm), kDecThreads, L::kSmem, st, 1, mk, mv, p);
 }
 
@@ -280,8 +280,8 @@ int launch_decode(const xattn_cache* c, DecodeParams& p, const DecodePlan& d, cu
                              std::max<long long>(1, 148 * 16 / pairs));
   }
   const long long blocks = (long long)c->B * p.Hq + wb * c->B * c->Hkv;
-  return launch(decode_join_kernel<C>, dim3((unsigned)blocks), kJoinThreads, 0, st, 1, p, d.rows,
-                8 * d.NT, (int)wb);
+  auto join = p.n_new != nullptr ? decode_join_kernel<C, true> : decode_join_kernel<C, false>;
+  return launch(join, dim3((unsigned)blocks), kJoinThreads, 0, st, 1, p, d.rows, 8 * d.NT, (int)wb);
 }
 
 // ------------------------------------------------------------------ evict
@@ -388,7 +388,6 @@ int xattn_decode_attn_ex(const xattn_heads* Q, const xattn_cache* cache, const i
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeParams p = {};
   p.cache = view_of(cache);
-  p.cache.n_new = n_new;
   p.q = static_cast<const bf16*>(Q->data);
   p.q_sb = Q->stride_b;
   p.q_sh = Q->stride_h;
@@ -403,6 +402,7 @@ int xattn_decode_attn_ex(const xattn_heads* Q, const xattn_cache* cache, const i
   p.G = Q->heads / cache->Hkv;
   p.HT = d.HT;
   p.scale_log2 = softmax_scale * kLog2e;
+  p.n_new = n_new;
   if (cache->C == 64) return launch_decode<64>(cache, p, d, as_stream(stream));
   return launch_decode<128>(cache, p, d, as_stream(stream));
 }

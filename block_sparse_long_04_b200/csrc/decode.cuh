@@ -77,6 +77,19 @@ struct DecodeParams {
   float* acc_out;          // [num_pages, Hkv, page] or null
   int Hq, G, HT;           // query heads, per kv head, head tiles per kv head
   float scale_log2;
+  const int32_t* n_new;    // [B] (IDLE kernels)
+
+  // Slots of sequence b that are attended to: none without a new token. (Kernels of their own
+  // for n_new, because a test of the pointer here cost 0.4 us of a short context's 6.8.)
+  template <bool IDLE>
+  __device__ __forceinline__ int length(int b) const {
+    const int n = cache.length(b);
+    return IDLE && n_new[b] != 1 ? 0 : n;
+  }
+  template <bool IDLE>
+  __device__ __forceinline__ bool valid(int b) const {
+    return cache.length_valid(b) && !(IDLE && (unsigned)n_new[b] > 1u);
+  }
 };
 
 // Keys per tile: 64, or 128 where a 32 KB stage holds them: a warp then works on two
@@ -105,15 +118,15 @@ struct Decode {
 };
 
 // ------------------------------------------------------------ the linear order
-template <int KEYS>
-__device__ __forceinline__ int dec_tiles(const CacheView& c, int b) {
-  return (c.length(b) + KEYS - 1) / KEYS;
+template <int KEYS, bool IDLE>
+__device__ __forceinline__ int dec_tiles(const DecodeParams& p, int b) {
+  return (p.length<IDLE>(b) + KEYS - 1) / KEYS;
 }
 // sum of the tiles of all sequences (one warp)
-template <int KEYS>
-__device__ __forceinline__ long long dec_total(const CacheView& c, int lane) {
+template <int KEYS, bool IDLE>
+__device__ __forceinline__ long long dec_total(const DecodeParams& p, int lane) {
   long long n = 0;
-  for (int b = lane; b < c.B; b += 32) n += dec_tiles<KEYS>(c, b);
+  for (int b = lane; b < p.cache.B; b += 32) n += dec_tiles<KEYS, IDLE>(p, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n;
@@ -124,11 +137,11 @@ struct DecPos {
   int b, hk, tile, tiles;
 };
 // Place of linear tile t (0 <= t < total * per), `per` items per sequence (one warp).
-template <int KEYS>
-__device__ __forceinline__ DecPos dec_find(const CacheView& c, long long t, int per, int lane) {
+template <int KEYS, bool IDLE>
+__device__ __forceinline__ DecPos dec_find(const DecodeParams& dp, long long t, int per, int lane) {
   long long base = 0;
-  for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const int n = b0 + lane < c.B ? dec_tiles<KEYS>(c, b0 + lane) : 0;
+  for (int b0 = 0; b0 < dp.cache.B; b0 += 32) {
+    const int n = b0 + lane < dp.cache.B ? dec_tiles<KEYS, IDLE>(dp, b0 + lane) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -154,14 +167,14 @@ __device__ __forceinline__ DecPos dec_find(const CacheView& c, long long t, int 
   return none;
 }
 // the next item with a tile (there is one)
-template <int KEYS>
-__device__ __forceinline__ void dec_next_item(const CacheView& c, DecPos& p, int per) {
+template <int KEYS, bool IDLE>
+__device__ __forceinline__ void dec_next_item(const DecodeParams& dp, DecPos& p, int per) {
   p.tile = 0;
   if (++p.hk < per) return;
   p.hk = 0;
   do {
     ++p.b;
-    p.tiles = p.b < c.B ? dec_tiles<KEYS>(c, p.b) : 1;
+    p.tiles = p.b < dp.cache.B ? dec_tiles<KEYS, IDLE>(dp, p.b) : 1;
   } while (p.tiles == 0);
 }
 
@@ -236,7 +249,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 }
 
 // ------------------------------------------------------------------ split
-template <int C, bool FP8, int NT>
+template <int C, bool FP8, int NT, bool IDLE>
 __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
 decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV,
@@ -269,12 +282,12 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
   }
   grid_dependency_wait();
   // every warp finds the CTA's share for itself
-  const long long total = dec_total<L::kKeys>(p.cache, lane) * per;
+  const long long total = dec_total<L::kKeys, IDLE>(p, lane) * per;
   const long long n_cta = total < gridDim.x ? total : gridDim.x;
   if ((long long)blockIdx.x >= n_cta) return;
   const long long t0 = blockIdx.x * total / n_cta;
   const int mine = (int)((blockIdx.x + 1) * total / n_cta - t0);
-  DecPos at = dec_find<L::kKeys>(p.cache, t0, per, lane);
+  DecPos at = dec_find<L::kKeys, IDLE>(p, t0, per, lane);
   __syncthreads();
 
   // a page holds a tile (or two), or a tile spans several pages
@@ -287,11 +300,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
     // lane l < n_parts looks up the page of part l, one tile ahead of its load
     auto page_of = [&](const DecPos& q) -> int {
       const int slot = q.tile * L::kKeys + (lane << part_log2);
-      if (lane >= n_parts || slot >= p.cache.length(q.b)) return -1;
+      if (lane >= n_parts || slot >= p.length<IDLE>(q.b)) return -1;
       return p.cache.page_table[(long long)q.b * p.cache.max_pages + (slot >> p.cache.page_log2)];
     };
     auto advance = [&](DecPos& q) {
-      if (++q.tile == q.tiles) dec_next_item<L::kKeys>(p.cache, q, per);
+      if (++q.tile == q.tiles) dec_next_item<L::kKeys, IDLE>(p, q, per);
     };
     int pid = page_of(at);
     int n = 0;
@@ -299,7 +312,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
       const DecPos cur = at;
       const int st = n % ST;
       const int slot = cur.tile * L::kKeys + (lane << part_log2);
-      const bool wanted = lane < n_parts && slot < p.cache.length(cur.b);
+      const bool wanted = lane < n_parts && slot < p.length<IDLE>(cur.b);
       const bool good = wanted && pid >= 0 && pid < p.cache.num_pages;
       const int row = (((pid * p.cache.Hkv) + cur.hk / p.HT) << p.cache.page_log2) +
                       (slot & ((1 << p.cache.page_log2) - 1));
@@ -371,7 +384,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
   bool ok = true;
   int n = 0;
   while (n < mine) {
-    const int len = p.cache.length(at.b);
+    const int len = p.length<IDLE>(at.b);
     const int kvh = at.hk / p.HT, ht = at.hk - kvh * p.HT;
     const int h0 = kvh * p.G + ht * 16;                     // first query head of the item
     const int heads = min(p.G - ht * 16, L::kRows);
@@ -724,7 +737,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
       if (at.tile == 0) p.seg[item].x = blockIdx.x;
       if (at.tile + seg_tiles == at.tiles) p.seg[item].y = blockIdx.x;
     }
-    if (n < mine) dec_next_item<L::kKeys>(p.cache, at, per);
+    if (n < mine) dec_next_item<L::kKeys, IDLE>(p, at, per);
   }
 }
 
@@ -756,7 +769,7 @@ __device__ __forceinline__ float2 dec_row_stat(const float2* ml, int rows, int n
 // of latencies (segment, statistics and values, sum): each warp takes every fourth partial,
 // a lane C/32 columns of it, and the values are loaded before the statistics that weigh them
 // are known.
-template <int C>
+template <int C, bool IDLE>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_per_tile,
                    int weight_blocks) {
@@ -773,13 +786,13 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
     const int kvh = h / p.G, g = h - kvh * p.G;
     const int item = b * per + kvh * p.HT + g / heads_per_tile;
     const int row = g % heads_per_tile;
-    const int len = p.cache.length(b);
+    const int len = p.length<IDLE>(b);
     const int2 seg = p.seg[item];      // not written for a sequence without keys
     if (len == 0) {                    // no key: o = 0, lse = -inf
       if (tid < C) p.O[(long long)bh * C + tid] = __float2bfloat16(0.f);
       if (tid == 0) {
         if (p.lse != nullptr) p.lse[bh] = kNegInf;
-        if (!p.cache.length_valid(b)) raise_device_error(kErrInvalid);
+        if (!p.valid<IDLE>(b)) raise_device_error(kErrInvalid);
       }
       return;
     }
@@ -835,7 +848,7 @@ decode_join_kernel(const __grid_constant__ DecodeParams p, int rows, int heads_p
   const int wb = blockIdx.x - n_join;
   const int pair = wb / weight_blocks, first = wb - pair * weight_blocks;
   const int b = pair / p.cache.Hkv, kvh = pair - b * p.cache.Hkv;
-  const int len = p.cache.length(b);
+  const int len = p.length<IDLE>(b);
   if (first * (kJoinThreads * 4) >= len) return;
   const int cap = p.cache.capacity();
   const float* logits = p.logits + ((long long)b * Hq + kvh * p.G) * cap;

@@ -46,19 +46,17 @@ struct CacheView {
   int32_t* ordinal;
   const int32_t* page_table;
   const int32_t* lens;
-  const int32_t* n_new;     // decoding: [B], sequences without a new token count as empty; or null
   int B, Hkv, page_log2, num_pages, max_pages;
 
   __device__ __forceinline__ int capacity() const { return max_pages << page_log2; }
   // Plain loads throughout: the read-only path must not be used for what an earlier kernel
   // wrote while this one was already being set up (see grid_dependency_wait).
   __device__ __forceinline__ bool length_valid(int b) const {
-    return lens[b] >= 0 && lens[b] <= capacity() && (n_new == nullptr || (unsigned)n_new[b] <= 1u);
+    return lens[b] >= 0 && lens[b] <= capacity();
   }
   // slots of sequence b; 0 for a length that its table cannot hold
   __device__ __forceinline__ int length(int b) const {
     const int n = lens[b];
-    if (n_new != nullptr && n_new[b] != 1) return 0;
     return n <= capacity() ? max(n, 0) : 0;
   }
   // index of (slot, kv head) in a [num_pages, Hkv, page] pool, -1 for a bad page id;
