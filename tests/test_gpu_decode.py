@@ -850,6 +850,32 @@ def test_decode_step_with_idle_sequences(e4m3):
         assert (o == 0).all() and torch.isneginf(bufs.lse).all() and same_cache(c, before)
 
 
+def test_captured_step_with_changing_idle_sequences():
+    """One capture of a step serves every later batch: which sequences are idle is read on the device."""
+    Hq, Hkv, C, B = 4, 2, 64, 3
+    start = make_cache(62, [40, 7, 200], Hkv, C, 16)
+    c = clone_cache(start)
+    x = torch.randn(B, 1, Hq + 2 * Hkv, C, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    q, k, v = (t.transpose(1, 2) for t in x.split([Hq, Hkv, Hkv], 2))
+    rot, pos, go = xa.Rotary.make((32,)), (c.lens - 1).view(B, 1, 1), torch.ones(B, dtype=torch.int32, device="cuda")
+    bufs = xa.DecodeBuffers.allocate(c, Hq, weights=True, with_lse=True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        xa.xattn_decode_step(q, k, v, pos, rot, c, bufs, weights=True, n_new=go)
+    for which in ([1, 1, 1], [0, 1, 0], [0, 0, 0], [1, 0, 1]):
+        go.copy_(torch.tensor(which))
+        for a, b in ((c.k_pages, start.k_pages), (c.v_pages, start.v_pages), (c.acc, start.acc),
+                     (c.ordinal, start.ordinal)):
+            a.copy_(b)
+        bufs.O.fill_(float("nan"))
+        g.replay()
+        want, wbufs = clone_cache(start), xa.DecodeBuffers.allocate(c, Hq, weights=True, with_lse=True)
+        xa.xattn_decode_step(q, k, v, pos, rot, want, wbufs, weights=True, n_new=go.clone())
+        assert torch.equal(bufs.O, wbufs.O) and torch.equal(bufs.lse, wbufs.lse) and same_cache(c, want)
+        for b in range(B):
+            assert (bufs.O[b] == 0).all() == (not which[b])
+
+
 def test_on_a_side_stream_and_in_graphs():
     """A decoding step captured into a graph and replayed with new inputs, lengths and pages,
     next to another graph with a workspace of its own."""
