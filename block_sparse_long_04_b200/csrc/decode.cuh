@@ -2,9 +2,12 @@
 //
 //   o_h = sum_j softmax_j(scale q_h . k_j) v_j,  j over the slots < lens[b]
 //
-// Bound. Every cached byte is used once for 2 * Hq/Hkv flops per bf16 element, so HBM
-// sets the pace (4 to 16 flops per byte at the usual group sizes). The kernel's task is
-// to keep enough bytes in flight on every SM and to stay off everybody's critical path.
+// Bound. A cached element is used for 2 flops per query head of its kv head: 4 to 16 flops per
+// byte of bf16 pages, 8 to 32 of e4m3 pages at 4 to 16 heads. Up to 16 heads every cached byte
+// is loaded once, and HBM sets the pace (for e4m3 with more than 8 heads, the instructions).
+// Larger groups are items of 16 heads each, which load K and V again at other times:
+// 32 heads per kv head take about twice, 128 eight times as long as 16. The kernel's task is to keep
+// enough bytes in flight on every SM and to stay off everybody's critical path.
 //
 // Split. The tiles (64 or 128 keys) of all (sequence, kv head) items form one linear order,
 // which is cut into equal shares, one per CTA: ragged batches and single long sequences
@@ -37,11 +40,13 @@
 // neighbour, and took 159 us instead of 136 for 32 sequences of 8192 slots with 16 heads per kv head.)
 // Sums, logits and statistics are fp32, o is rounded once.
 //
-// Measured, whole calls, 32 query and 8 kv heads, C = 128: one sequence of 131072 bf16 slots
-// 85 us (0.54 GB, 6.3 TB/s), 32 ragged e4m3 sequences 94 us (0.59 GB, 6.2 TB/s), 8 of 32768
-// with weights 184 us (1.09 GB, 5.9 TB/s), one of 777 slots 6.8 us; 16 heads per kv head
-// 87 us for the first case. What binds is HBM; for e4m3 the widening (64 of 290
-// instructions per 16 keys and warp) comes close.
+// Measured, whole calls, 32 query and 8 kv heads, C = 128 (a range is over several GPUs): one
+// sequence of 131072 bf16 slots 85 to 88 us (0.54 GB, 6.1 to 6.3 TB/s), 32 ragged e4m3 sequences
+// 95 us (0.59 GB, 6.1 TB/s), 8 of 32768 with weights 185 to 189 us (1.09 GB, 5.8 TB/s), one of 777
+// slots 6.8 us. 16 heads per kv head: 90 us for the first case in bf16, 71 to 82 us in e4m3 (half the
+// bytes). One kv head, 32 sequences of 32768 slots (0.54 GB in bf16, 0.27 in e4m3): 32 query heads
+// 168 and 132 us, 128 query heads 620 and 500 us. What binds up to 8 heads is HBM; for e4m3 the
+// widening (64 of some 260 instructions per 16 keys and warp) comes close.
 //
 // Keys behind the end of a sequence inside its last page are masked, and their V rows
 // are zeroed in shared memory before use: 0 * NaN of a stale row would not be 0.
@@ -236,7 +241,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 __device__ __forceinline__ void bar_mma_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Cached rows are read once per call: first to leave L2, where the partials, logits and
+// Cached rows are read once per call and head tile: first to leave L2, where the partials, logits and
 // queries should stay (128K keys 86.6 -> 84.5 us, ragged e4m3 batch 103.3 -> 100.4 us).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, uint64_t* bar) {

@@ -13,8 +13,9 @@
 // Selection: a radix search for the n-th smallest key, 11 + 11 + 10 bits, where the key
 // is the weight's order-preserving bit pattern, inverted (ascending key = descending
 // weight), and 0 for a safe slot. One cluster of 1 to 8 CTAs per row: each CTA reads its
-// part of the weights and ordinals once, keeps the keys in shared memory (or, if they do
-// not fit, in the workspace),
+// part of the weights and ordinals once, keeps the keys in shared memory (or, if those of the
+// table's capacity do not fit, in the workspace: 128 rows of 4224 slots take 14.8 us in a
+// table of 131088 slots, 13.8 in one of 4224),
 // and adds the bins that hold anything to the first CTA's through distributed shared memory;
 // that one finds the digit and the others read it. Inside a CTA
 // every warp owns a run of neighbouring slots, so that the last step, which writes the two
@@ -22,7 +23,7 @@
 // bound by latencies (a row is a few KB to 1 MB, and each of its ~20 dependent steps is a
 // memory or barrier latency), not by bandwidth; its loops are kept short and rolled, since
 // code that runs once per CTA is fetched once per CTA too. 8 rows of 131072 slots (64 CTAs)
-// take 25 us of the call's 74, 128 rows of 4224 slots 12 of its 14. Everything is counted in
+// take 25 us of the call's 73, 128 rows of 4224 slots 12 of its 14. Everything is counted in
 // integers: the result does not depend on the order of the atomics.
 #pragma once
 #include "common.cuh"

@@ -19,8 +19,10 @@
 // strided copy with 16 products in it, four rows in flight. What the loop must not hold is
 // address arithmetic: with it, and the sines read per row, a 32K prompt of 32 + 8 heads
 // took 180 us, 120 us with the sines in registers, 107 us so (0.67 GB, 6.2 TB/s; the
-// 118784-token layer of 24 + 24 heads 437 us, 6.7 TB/s; 32K tokens of 8 heads into e4m3 pages
-// 38 us, 5.3 TB/s). Two resident CTAs with four rows in flight and three with two measured
+// 118784-token layer of 24 + 24 heads 437 us, 6.7 TB/s; 32K tokens of 8 heads into bf16 pages
+// 44 us, 6.1 TB/s, into e4m3 pages 38 us, 5.3 TB/s; rotated with 32 query heads on the way 129 us
+// into either). The e4m3 instance without rotation is held to 64 registers and spills 100 bytes
+// of them. Two resident CTAs with four rows in flight and three with two measured
 // alike, more CTAs slower.
 //
 // Append. Token t of sequence b goes to slot lens[b] - n_new[b] + t; its page and row

@@ -336,8 +336,8 @@ XATTN_API int xattn_dense_attn(const void* Q, const void* K, const void* V,
  *   - The structs are read by the host during the call and may be reused at once.
  *     Every pointer inside them is device memory, save that of the struct itself.
  *   - lens, page_table, n_new, seen and pos are read on the device. A length outside
- *     [0, max_pages * page] (it counts as 0), a page id outside [0, num_pages) that a
- *     length reaches (its slots are left out), or an n_new outside [0, min(T, lens)] (it
+ *     [0, max_pages * page] (it counts as 0), a page id outside [0, num_pages) of a slot
+ *     that the call reads or writes (the slot is left out), or an n_new outside [0, min(T, lens)] (it
  *     counts as 0) raises XATTN_EINVAL in the device error word; nothing outside the given
  *     buffers is read or written. Table entries behind a sequence's last page are never
  *     read as pages and may hold anything.
@@ -426,7 +426,7 @@ typedef struct {
  *   n_new  int32 [B], or NULL for T new tokens everywhere
  *   seen   int32 [B], tokens of the sequence so far including the new ones (more than
  *          lens once tokens were evicted), or NULL for lens
- * e4m3 pages take x / scale, rounded once to nearest and saturated at +-448.
+ * e4m3 pages take the fp32 quotient x / scale, rounded to nearest and saturated at +-448.
  */
 XATTN_API int xattn_cache_append(const xattn_heads* K, const xattn_heads* V,
                                  const xattn_cache* cache, int T, const int32_t* n_new,
@@ -452,7 +452,8 @@ XATTN_API size_t xattn_decode_workspace_size(const xattn_cache* cache, int Hq, i
  * slots s < lens[b]:
  *   O[b,h] = sum_s p_s v_s,  p = softmax(softmax_scale * q_h . k_s),
  * with K and V of head h / (Hq/Hkv). A sequence of length 0 gets O = 0, lse = -inf.
- *   Q        [B, Hq, 1, C] at its strides (stride_m is not used); Hq/Hkv <= 128
+ *   Q        [B, Hq, 1, C] at its strides (stride_m is not used); Hq/Hkv <= 128. (Beyond 16
+ *            the cache is loaded once per 16 query heads of a kv head.)
  *   O        bf16 [B, Hq, C], dense
  *   lse      fp32 [B, Hq], natural-log log-sum-exp, or NULL
  *   acc_out  fp32 [num_pages, Hkv, page] or NULL: acc_out = acc + sum of p over the query
@@ -493,6 +494,9 @@ XATTN_API size_t xattn_cache_evict_workspace_size(const xattn_cache* cache, int 
  * counts as larger than +inf. A kept slot below n stays in place; the i-th evicted slot
  * below n (ascending) takes the row, acc and ordinal of the i-th kept slot from the end.
  * The order of slots carries no meaning for xattn_decode_attn; ordinals tell the tokens.
+ * acc holds what decoding steps with acc_out have added since the append cleared it; the
+ * prefill adds nothing. Straight after a prompt all of it is 0, and the ties keep the
+ * safe slots and the prompt's first: fill acc, or decode with weights, before evicting.
  * lens is not changed, because layers may share it: clamp it to budget after the last
  * layer. Slots from n on are left as they were. Slots of a bad page (see above) have no
  * rows: those below n keep their places, and the others are chosen for the rest.
