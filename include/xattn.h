@@ -337,10 +337,10 @@ XATTN_API int xattn_dense_attn(const void* Q, const void* K, const void* V,
  *     Every pointer inside them is device memory, save that of the struct itself.
  *   - lens, page_table, n_new, seen and pos are read on the device. A length outside
  *     [0, max_pages * page] (it counts as 0), a page id outside [0, num_pages) of a slot
- *     that the call reads or writes (the slot is left out), or an n_new outside [0, min(T, lens)] (it
- *     counts as 0) raises XATTN_EINVAL in the device error word; nothing outside the given
- *     buffers is read or written. Table entries behind a sequence's last page are never
- *     read as pages and may hold anything.
+ *     that the call reads or writes (the slot is left out), or an n_new outside
+ *     [0, min(T, lens)] (it counts as 0) raises XATTN_EINVAL in the device error word;
+ *     nothing outside the given buffers is read or written. Table entries behind a
+ *     sequence's last page are never read as pages and may hold anything.
  *   - Calls are ordered by their stream like any other work. (They are set up while the
  *     kernel ahead of them still runs, and wait for its end before their first read.)
  *   - A page belongs to one (sequence, position in its table) for every call that
